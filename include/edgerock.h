@@ -281,6 +281,85 @@ int er_linear(const er_bf16* x, int32_t T, const er_bf16* w, int32_t F, int32_t 
               int32_t y_fp32, int32_t ldy, void* ws, size_t ws_bytes, int32_t* dev_error,
               er_stream_t stream);
 
+/* The products that stand between the SWA∥RMA layers of the model [F-arch],
+ * beside er_linear: any T, F and strides, with their epilogue fused.
+ *   er_linear_fused: y = act(x·wᵀ + bias) + residual
+ *   er_gated_linear: y = act(x·w_gateᵀ) ⊙ (x·w_upᵀ), the gated feed-forward
+ *                    block up to its down projection, in one kernel (the down
+ *                    projection and the residual are an er_linear_fused call)
+ * x BF16 [T][ldx], K values of a row used; w, w_gate, w_up BF16 [F][K]
+ * (row-major, the nn.Linear layout); bias BF16 [F] or NULL; y BF16 (y_fp32 = 0,
+ * round to nearest even) or FP32 (y_fp32 = 1), [T][ldy]; residual NULL or of
+ * y's type, [T][ldr], and may be y itself (ldr = ldy).  BF16 products, sums,
+ * bias, activation, gate product and residual are FP32 and rounded once, into
+ * y.  Activations: ER_ACT_*.
+ *  T >= 0 (0: nothing is enqueued), F >= 1, K >= 8 and a multiple of 8, ldx >= K
+ *  and a multiple of 8, ldy and ldr >= F; x, w, w_gate, w_up 16-byte aligned, the
+ *  other pointers aligned to their elements; y overlaps no input but a residual
+ *  equal to it.  Columns from F on of y are left as they are.  No workspace.
+ *  The summation order is fixed for given sizes and alignments: the same inputs
+ *  give the same bits.  A bounded wait that gives up records ER_ETIMEOUT in
+ *  *dev_error (NULL: the library's own word, er_last_call_error).
+ * The gated product holds act(gate) * up for infinite and NaN values as IEEE
+ * arithmetic gives it; SiLU and the GELUs of -inf are NaN (their formula's
+ * inf * 0). */
+#define ER_ACT_NONE 0
+#define ER_ACT_SILU 1      /* v / (1 + e^-v) */
+#define ER_ACT_GELU 2      /* v/2 · (1 + erf(v / sqrt(2))) */
+#define ER_ACT_GELU_TANH 3 /* v/2 · (1 + tanh(sqrt(2/pi)·(v + 0.044715·v^3))) */
+int er_linear_fused(const er_bf16* x, int32_t ldx, int32_t T, const er_bf16* w, int32_t F,
+                    int32_t K, const er_bf16* bias, int32_t act, const void* residual,
+                    int32_t ldr, void* y, int32_t y_fp32, int32_t ldy, int32_t* dev_error,
+                    er_stream_t stream);
+int er_gated_linear(const er_bf16* x, int32_t ldx, int32_t T, const er_bf16* w_gate,
+                    const er_bf16* w_up, int32_t F, int32_t K, int32_t act, void* y,
+                    int32_t y_fp32, int32_t ldy, int32_t* dev_error, er_stream_t stream);
+
+/* Linear attention with a decay for each head: the reads and state updates of a
+ * recurrent layer, whose state is a matrix of fixed size for each head whatever
+ * the stream's length [F-arch], [F-mem].  Per value head
+ *   S_t = e^{g_t} S_{t-1} + k_t v_tᵀ,   o_t = scale · S_tᵀ q_t
+ * (a token reads its own k and v), with g = log_decay.
+ *   state  FP32 [s_max][v_heads][k_dim][v_dim], caller-owned, updated in place;
+ *          zero for a stream's start.  Sequence b of a call is row seq_ids[b]
+ *          (device int32 [B]); rows not listed are left as they are.
+ *   q, k   BF16 rows of [k_heads][k_dim] values, ldq / ldk apart; v rows of
+ *          [v_heads][v_dim], ldv apart: they may be slices of one projection.
+ *          Value head h reads q and k of head h / (v_heads / k_heads).
+ *   log_decay FP32 rows of [v_heads] natural logs, ldg apart, or ldg = 0: one
+ *          row for every token.  Any value but +inf: 0 keeps the state, -inf
+ *          forgets it (values below -1000 count as -inf), NaN spreads as in the
+ *          formula.
+ *   o      BF16 rows of [v_heads][v_dim], ldo apart, rounded once.
+ * er_decay_decode: one token for each of B sequences, row b the token of
+ * sequence b.  er_decay_prefill: the tokens of sequence b are rows
+ * [cu_tokens[b], cu_tokens[b + 1]) (device int32 [B + 1]) of T packed rows;
+ * empty sequences keep their state; rows outside every sequence are left as
+ * they are in o.  A sequence's tokens may be cut into calls anywhere.
+ *  v_heads a multiple of k_heads, at most 4096; k_dim, v_dim 64 or 128; 0 <= B <=
+ *  s_max (larger: ER_ECAPACITY), B <= 65535; row strides multiples of 8 and at
+ *  least a row; state, q, k, v, o 16-byte aligned; ws 256-byte aligned, at least
+ *  er_decay_prefill_workspace_bytes(shape, B, T) (0 for bad sizes).  o overlaps no
+ *  input.  A sequence whose state row is out of range or was listed before it in
+ *  the call, or whose rows leave [0, T), is skipped (its state and its rows of
+ *  o are left as they are) and records ER_EINVAL in *dev_error (NULL: the library's
+ *  own word, er_last_call_error).  The same inputs give the same bits. */
+typedef struct er_decay_shape {
+  int32_t k_heads, v_heads, k_dim, v_dim;
+} er_decay_shape;
+size_t er_decay_prefill_workspace_bytes(const er_decay_shape* shape, int32_t B, int32_t T);
+int er_decay_decode(float* state, int32_t s_max, const int32_t* seq_ids, int32_t B,
+                    const er_decay_shape* shape, const er_bf16* q, int32_t ldq, const er_bf16* k,
+                    int32_t ldk, const er_bf16* v, int32_t ldv, const float* log_decay,
+                    int32_t ldg, float scale, er_bf16* o, int32_t ldo, int32_t* dev_error,
+                    er_stream_t stream);
+int er_decay_prefill(float* state, int32_t s_max, const int32_t* seq_ids,
+                     const int32_t* cu_tokens, int32_t B, int32_t T, const er_decay_shape* shape,
+                     const er_bf16* q, int32_t ldq, const er_bf16* k, int32_t ldk,
+                     const er_bf16* v, int32_t ldv, const float* log_decay, int32_t ldg,
+                     float scale, er_bf16* o, int32_t ldo, void* ws, size_t ws_bytes,
+                     int32_t* dev_error, er_stream_t stream);
+
 /* a3 — retention scores [F-arch], [N-rma]: s = W2 · SiLU(W1 · x) with FP32
  * accuracy: W1 is taken as three BF16 terms hi + mid + lo (residual below
  * 2^-24 |W1|), each product with the BF16 x is exact and accumulates in FP32;

@@ -14,6 +14,7 @@ in that library's kernels.  torch provides device memory and streams only.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -27,6 +28,8 @@ __all__ = ["State", "LayerWeights", "qk_norm_rope", "rma_score", "rma_append_pen
            "profile_read", "decode_workspace_bytes", "prefill_workspace_bytes",
            "attend_workspace_bytes", "score_workspace_bytes", "rma_score_noalloc",
            "wait_selftest", "last_call_error", "linear", "linear_workspace_bytes",
+           "linear_fused", "gated_linear", "decay_decode", "decay_prefill",
+           "decay_prefill_workspace_bytes",
            "ERError"]
 
 
@@ -236,6 +239,204 @@ def linear(x: torch.Tensor, w: torch.Tensor, fp32_out: bool = False, out=None, w
         dev_ptr(x, torch.bfloat16, "x"), T, dev_ptr(w, torch.bfloat16, "w"), F, K,
         dev_ptr(out, dt, "out"), 1 if fp32_out else 0, out.stride(0), dev_ptr(ws), ws.numel(),
         err, stream_handle(stream, x.device)))
+    return out
+
+
+def _device_of(x: torch.Tensor, name: str):
+    """The device of a call's tensors (that of its first one)."""
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return x.device
+
+
+def _on_stream(f):
+    """`stream=`: run the call with that stream as the current one, so that what it
+    allocates belongs to the stream that uses it."""
+    @functools.wraps(f)
+    def g(first, *args, stream=None, **kw):
+        if stream is None:
+            return f(first, *args, **kw)
+        if stream.device != first.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {first.device}")
+        with torch.cuda.stream(stream):
+            return f(first, *args, **kw)
+    return g
+
+
+def _call(fn: str, device, *args):
+    """Call a C entry point on its tensors' device and that device's current stream."""
+    f = getattr(lib(), fn)
+    s = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        rc = f(*args, s)
+    else:
+        with torch.cuda.device(device):
+            rc = f(*args, s)
+    if rc != 0:
+        raise ERError(fn, rc)
+
+
+def _arg(t, device, dtype, shape, name):
+    """The address of a tensor whose last dimensions are dense and whose rows
+    (dimension 0) may be strided, and that row stride in elements."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    st = t.stride()
+    dense = 1
+    for n, d in zip(reversed(shape[1:]), reversed(st[1:])):
+        if d != dense and n != 1:
+            raise ValueError(f"{name} must have dense rows, got strides {st}")
+        dense *= n
+    # a single row's stride says nothing
+    ld = st[0] if shape[0] > 1 else dense
+    if ld < dense:
+        raise ValueError(f"{name} must not have overlapping rows, got strides {st}")
+    return t.data_ptr(), ld
+
+
+def _dense(t, device, dtype, shape, name):
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _act(act) -> int:
+    code = _lib.ACTS.get("none" if act is None else act)
+    if code is None:
+        raise ValueError(f"act must be one of {sorted(_lib.ACTS)}, got {act!r}")
+    return code
+
+
+def _error_word(dev_error, device):
+    return None if dev_error is None else _dense(dev_error, device, torch.int32, dev_error.shape,
+                                                 "dev_error")
+
+
+@_on_stream
+def linear_fused(x: torch.Tensor, w: torch.Tensor, bias=None, act=None, residual=None,
+                 fp32_out: bool = False, out=None, dev_error=None):
+    """y = act(x · wᵀ + bias) + residual (er_linear_fused): x BF16 [T, K] (rows may be
+    strided), w BF16 [F, K], bias BF16 [F]; y and residual BF16 (or FP32 with fp32_out)
+    [T, F], rows may be strided, residual may be out itself; act None / "none", "silu",
+    "gelu" or "gelu_tanh"."""
+    device = _device_of(x, "x")
+    T, K = x.shape
+    F = w.shape[0]
+    bf = torch.bfloat16
+    dt = torch.float32 if fp32_out else bf
+    if out is None:
+        out = torch.empty(T, F, dtype=dt, device=device)
+    px, ldx = _arg(x, device, bf, (T, K), "x")
+    py, ldy = _arg(out, device, dt, (T, F), "out")
+    pr, ldr = (None, F) if residual is None else _arg(residual, device, dt, (T, F), "residual")
+    _call("er_linear_fused", device, px, ldx, T, _dense(w, device, bf, (F, K), "w"), F, K,
+          None if bias is None else _dense(bias, device, bf, (F,), "bias"), _act(act), pr, ldr,
+          py, 1 if fp32_out else 0, ldy, _error_word(dev_error, device))
+    return out
+
+
+@_on_stream
+def gated_linear(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act="silu",
+                 fp32_out: bool = False, out=None, dev_error=None):
+    """y = act(x · w_gateᵀ) ⊙ (x · w_upᵀ) (er_gated_linear): the gated feed-forward block up to
+    its down projection, which is a linear_fused call.  x BF16 [T, K] (rows may be strided),
+    w_gate and w_up BF16 [F, K] (the halves of one stacked [2F, K] weight are such), y BF16
+    (or FP32 with fp32_out) [T, F], rows may be strided; act as in linear_fused."""
+    device = _device_of(x, "x")
+    T, K = x.shape
+    F = w_gate.shape[0]
+    bf = torch.bfloat16
+    dt = torch.float32 if fp32_out else bf
+    if out is None:
+        out = torch.empty(T, F, dtype=dt, device=device)
+    px, ldx = _arg(x, device, bf, (T, K), "x")
+    py, ldy = _arg(out, device, dt, (T, F), "out")
+    _call("er_gated_linear", device, px, ldx, T,
+          _dense(w_gate, device, bf, (F, K), "w_gate"), _dense(w_up, device, bf, (F, K), "w_up"),
+          F, K, _act(act), py, 1 if fp32_out else 0, ldy, _error_word(dev_error, device))
+    return out
+
+
+def _decay_shape(state, q, v):
+    if state.dim() != 4 or q.dim() != 3 or v.dim() != 3:
+        raise ValueError("state must be [rows, v_heads, k_dim, v_dim], q, k [T, k_heads, k_dim], "
+                         "v [T, v_heads, v_dim]")
+    return _lib.CDecayShape(q.shape[1], *state.shape[1:])
+
+
+def _decay_rows(device, sh, T, q, k, v, log_decay, scale, out):
+    """The arguments q .. o of the decay calls, and out."""
+    bf = torch.bfloat16
+    qk, vo = (T, sh.k_heads, sh.k_dim), (T, sh.v_heads, sh.v_dim)
+    if out is None:
+        out = torch.empty(vo, dtype=bf, device=device)
+    if log_decay.dim() == 2 and T > 1 and log_decay.stride(0) == 0:
+        if log_decay.shape[0] != T:
+            raise ValueError(f"log_decay must have {T} rows, got {log_decay.shape[0]}")
+        log_decay = log_decay[0]  # one row, expanded
+    if log_decay.dim() == 1:
+        pg, ldg = _dense(log_decay, device, torch.float32, (sh.v_heads,), "log_decay"), 0
+    else:
+        pg, ldg = _arg(log_decay, device, torch.float32, (T, sh.v_heads), "log_decay")
+    return (*_arg(q, device, bf, qk, "q"), *_arg(k, device, bf, qk, "k"),
+            *_arg(v, device, bf, vo, "v"), pg, ldg,
+            sh.k_dim ** -0.5 if scale is None else scale, *_arg(out, device, bf, vo, "out")), out
+
+
+@_on_stream
+def decay_decode(state: torch.Tensor, seq_ids, q, k, v, log_decay, scale=None, out=None, dev_error=None):
+    """One token for each of B sequences through linear attention with a decay for each head
+    (er_decay_decode): S = e^g S + k vᵀ, o = scale · Sᵀ q.  state FP32 [rows, v_heads, k_dim,
+    v_dim], rows seq_ids updated in place; q, k BF16 [B, k_heads, k_dim], v BF16 [B, v_heads,
+    v_dim] (rows may be strided: slices of one projection), log_decay FP32 [B, v_heads] or
+    [v_heads]; scale defaults to k_dim ** -0.5; returns o BF16 [B, v_heads, v_dim]."""
+    device = _device_of(state, "state")
+    ids = _ids(seq_ids, device)
+    B = ids.numel()
+    sh = _decay_shape(state, q, v)
+    rows, out = _decay_rows(device, sh, B, q, k, v, log_decay, scale, out)
+    _call("er_decay_decode", device,
+          _dense(state, device, torch.float32, state.shape, "state"), state.shape[0],
+          ids.data_ptr(), B, sh, *rows, _error_word(dev_error, device))
+    return out
+
+
+def decay_prefill_workspace_bytes(k_heads: int, v_heads: int, k_dim: int, v_dim: int, B: int,
+                                  T: int) -> int:
+    return int(lib().er_decay_prefill_workspace_bytes(
+        _lib.CDecayShape(k_heads, v_heads, k_dim, v_dim), B, T))
+
+
+@_on_stream
+def decay_prefill(state: torch.Tensor, seq_ids, cu_tokens, q, k, v, log_decay, scale=None,
+                  out=None, ws=None, dev_error=None):
+    """The tokens of B prompts (or chunks of them) through linear attention with a decay for
+    each head (er_decay_prefill): sequence b's tokens are rows [cu_tokens[b], cu_tokens[b + 1])
+    of T packed rows of q, k, v, log_decay and out; the rest as in decay_decode, which it
+    equals token by token."""
+    device = _device_of(state, "state")
+    ids, cu = _ids(seq_ids, device), _ids(cu_tokens, device)
+    B, T = ids.numel(), q.shape[0]
+    if cu.numel() != B + 1:
+        raise ValueError(f"cu_tokens must have {B + 1} entries, got {cu.numel()}")
+    sh = _decay_shape(state, q, v)
+    rows, out = _decay_rows(device, sh, T, q, k, v, log_decay, scale, out)
+    nb = int(lib().er_decay_prefill_workspace_bytes(sh, B, T)) if B else 0
+    ws = _ws(nb, device, ws)
+    _call("er_decay_prefill", device,
+          _dense(state, device, torch.float32, state.shape, "state"), state.shape[0],
+          ids.data_ptr(), cu.data_ptr(), B, T, sh, *rows, ws.data_ptr(), ws.numel(),
+          _error_word(dev_error, device))
     return out
 
 

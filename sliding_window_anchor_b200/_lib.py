@@ -44,6 +44,16 @@ class CWeights(ctypes.Structure):
                                                "w1_split", "w_qkv_score")]
 
 
+class CDecayShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("k_heads", "v_heads", "k_dim", "v_dim")]
+
+
+ACTS = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3}  # ER_ACT_*
+
+
+_P, _I, _F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float
+_DECAY_ROWS = [_P, _I, _P, _I, _P, _I, _P, _I, _F, _P, _I]  # q, k, v, log_decay, scale, o
+
 EXPORTS = {
     # name: (restype, argtypes)
     "er_state_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
@@ -70,6 +80,14 @@ EXPORTS = {
                                  ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
                                  ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p,
                                  ctypes.c_void_p]),
+    "er_linear_fused": (ctypes.c_int, [_P, _I, _I, _P, _I, _I, _P, _I, _P, _I, _P, _I, _I, _P,
+                                       _P]),
+    "er_gated_linear": (ctypes.c_int, [_P, _I, _I, _P, _P, _I, _I, _I, _P, _I, _I, _P, _P]),
+    "er_decay_prefill_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(CDecayShape), _I, _I]),
+    "er_decay_decode": (ctypes.c_int, [_P, _I, _P, _I, ctypes.POINTER(CDecayShape), *_DECAY_ROWS,
+                                       _P, _P]),
+    "er_decay_prefill": (ctypes.c_int, [_P, _I, _P, _P, _I, _I, ctypes.POINTER(CDecayShape),
+                                        *_DECAY_ROWS, _P, ctypes.c_size_t, _P, _P]),
     "er_score_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32]),
     "er_score_split_w1": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
     "er_wait_selftest": (ctypes.c_int, [ctypes.POINTER(CState), ctypes.c_int32, ctypes.c_void_p]),
