@@ -293,8 +293,8 @@ int er_linear(const er_bf16* x, int32_t T, const er_bf16* w, int32_t F, int32_t 
  * y's type, [T][ldr], and may be y itself (ldr = ldy).  BF16 products, sums,
  * bias, activation, gate product and residual are FP32 and rounded once, into
  * y.  Activations: ER_ACT_*.
- *  T >= 0 (0: nothing is enqueued), F >= 1, K >= 8 and a multiple of 8, ldx >= K
- *  and a multiple of 8, ldy and ldr >= F; x, w, w_gate, w_up 16-byte aligned, the
+ *  T >= 0 (0: nothing is enqueued), F >= 1, K >= 8 and a multiple of 8, each at
+ *  most 2^30, ldx >= K and a multiple of 8, ldy and ldr >= F; x, w, w_gate, w_up 16-byte aligned, the
  *  other pointers aligned to their elements; y overlaps no input but a residual
  *  equal to it.  Columns from F on of y are left as they are.  No workspace.
  *  The summation order is fixed for given sizes and alignments: the same inputs

@@ -320,4 +320,9 @@ bool encode_store_2d(CUtensorMap* m, const void* base, bool fp32, uint64_t cols,
 bool encode_bf16_2d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows,
                     uint64_t pitch_bytes, uint32_t box_cols, uint32_t box_rows);
 
+// Host: the same for BF16 or FP32 rows, loads and stores with 128-byte swizzle,
+// encoded anew by every call.
+bool encode_rows(CUtensorMap* m, const void* base, bool fp32, uint64_t cols, uint64_t rows,
+                 uint64_t pitch_bytes, uint32_t box_cols, uint32_t box_rows);
+
 }  // namespace er
