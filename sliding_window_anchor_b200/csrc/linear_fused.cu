@@ -27,24 +27,32 @@ struct FusedParams {
   int act, f32;
 };
 
+// v / (1 + e^-z).  The quotient is __fdividef (2 ulp; 0 for a divisor above 2^126, where
+// the value is below 2^-118): a division rounded to nearest takes a slow path for
+// v = 0, the value of every row a tile has too many (gated, 9 tokens: 17 us a tile).
+__device__ __forceinline__ float times_sigmoid(float v, float z) {
+  return __fdividef(v, 1.f + __expf(-z));
+}
+
 __device__ __forceinline__ float activate(float v, int act) {
   switch (act) {
     case ER_ACT_SILU:
-      return v / (1.f + expf(-v));
+      return times_sigmoid(v, v);
     case ER_ACT_GELU:
       return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
     case ER_ACT_GELU_TANH:
-      return 0.5f * v * (1.f + tanhf(0.79788456080286536f * (v + 0.044715f * v * v * v)));
+      // 1 + tanh(z) = 2 / (1 + e^-2z)
+      return times_sigmoid(v, 1.5957691216057308f * (v + 0.044715f * v * v * v));
     default:
       return v;
   }
 }
 
 // One output value from its sums: v (+ u, the gated product's second one).
-__device__ __forceinline__ float finish(const FusedParams& P, float v, float u, bool gated, int t,
-                                        int f) {
+__device__ __forceinline__ float finish(const FusedParams& P, float v, float u, bool gated, int act,
+                                        int t, int f) {
   if (P.bias) v += bf1(P.bias[f]);
-  v = activate(v, P.act);
+  v = activate(v, act);
   if (gated) v *= u;
   if (P.residual)
     v += P.f32 ? static_cast<const float*>(P.residual)[t * P.ldr + f]
@@ -59,17 +67,38 @@ __device__ __forceinline__ void store_one(const FusedParams& P, int t, int f, fl
     static_cast<uint16_t*>(P.y)[t * P.ldy + f] = f2bf(v);
 }
 
-__device__ __forceinline__ void activate32(float (&v)[32], int act) {
-  // one branch for the 32 values
-  if (act == ER_ACT_SILU) {
+// Adds the residual to four values of token t, features f.., and stores them.
+__device__ __forceinline__ void finish_four(const FusedParams& P, int t, int f,
+                                            const float (&v)[4]) {
+  const bool all = f + 4 <= P.F;
+  const int64_t to = t * P.ldy + f, from = t * P.ldr + f;
+  if (P.f32) {
+    float* y = static_cast<float*>(P.y) + to;
+    const float* r = static_cast<const float*>(P.residual) + from;
+    if (all && ((uintptr_t)y & 15u) == 0 && (!P.residual || ((uintptr_t)r & 15u) == 0)) {
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (P.residual) a = *reinterpret_cast<const float4*>(r);
+      *reinterpret_cast<float4*>(y) =
+          make_float4(v[0] + a.x, v[1] + a.y, v[2] + a.z, v[3] + a.w);
+      return;
+    }
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = activate(v[i], ER_ACT_SILU);
-  } else if (act == ER_ACT_GELU) {
+    for (int j = 0; j < 4; ++j)
+      if (f + j < P.F) y[j] = v[j] + (P.residual ? r[j] : 0.f);
+  } else {
+    uint16_t* y = static_cast<uint16_t*>(P.y) + to;
+    const uint16_t* r = static_cast<const uint16_t*>(P.residual) + from;
+    if (all && ((uintptr_t)y & 7u) == 0 && (!P.residual || ((uintptr_t)r & 7u) == 0)) {
+      uint2 a = make_uint2(0u, 0u);
+      if (P.residual) a = *reinterpret_cast<const uint2*>(r);
+      *reinterpret_cast<uint2*>(y) =
+          make_uint2(pack_bf2(v[0] + bf_lo(a.x), v[1] + bf_hi(a.x)),
+                     pack_bf2(v[2] + bf_lo(a.y), v[3] + bf_hi(a.y)));
+      return;
+    }
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = activate(v[i], ER_ACT_GELU);
-  } else if (act == ER_ACT_GELU_TANH) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = activate(v[i], ER_ACT_GELU_TANH);
+    for (int j = 0; j < 4; ++j)
+      if (f + j < P.F) y[j] = f2bf(v[j] + (P.residual ? bf1(r[j]) : 0.f));
   }
 }
 
@@ -163,6 +192,13 @@ __device__ __forceinline__ uint4 ld_weights(const uint16_t* p) {
                : "l"(p));
   return r;
 }
+__device__ __forceinline__ uint4 ld_tokens(const uint16_t* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
 
 // D += A·B, m16n8k16, BF16 operands, FP32 accumulators.
 __device__ __forceinline__ void mma16816(float d[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -175,7 +211,7 @@ __device__ __forceinline__ void mma16816(float d[4], uint32_t a0, uint32_t a1, u
 }
 
 template <bool GATED>
-__global__ void __launch_bounds__(32 * FV_MAXW) k_fused_few(const FusedParams P) {
+__global__ void __launch_bounds__(32 * FV_MAXW, 2) k_fused_few(const FusedParams P) {
   constexpr int NW = GATED ? 2 : 1;  // weights
   constexpr int U = 8 / NW;          // K steps in flight
   __shared__ float red[FV_MAXW][NW][4][32];
@@ -193,33 +229,38 @@ __global__ void __launch_bounds__(32 * FV_MAXW) k_fused_few(const FusedParams P)
   float acc[NW][4] = {};
   grid_dep_wait();
   grid_dep_trigger();
-  for (int k0 = k_lo; k0 < k_hi; k0 += U) {
-    uint4 a[NW][U], b[NW][U], x[U];
-    // every load is issued; one outside the slice or K takes the row's start, and zero
+  // U steps of weights and tokens are in flight, carried around the loop (loads that
+  // are used in the iteration that issues them are moved down to their uses, one in
+  // flight at a time); a step outside the slice or K loads its row's start and counts
+  // as zero
+  uint4 a[U][NW], b[U][NW], x[U];
+  auto inside = [&](int step) { return step < k_hi && 32 * step + 8 * c < P.K; };
+  auto load = [&](int k0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k = 32 * (k0 + u) + 8 * c;
-      const bool in = k0 + u < k_hi && k < P.K;
-      const int at = in ? k : 0;
+      const int at = inside(k0 + u) ? 32 * (k0 + u) + 8 * c : 0;
 #pragma unroll
       for (int n = 0; n < NW; ++n) {
-        a[n][u] = ld_weights(wp[n] + ra + at);
-        b[n][u] = ld_weights(wp[n] + rb + at);
+        a[u][n] = ld_weights(wp[n] + ra + at);
+        b[u][n] = ld_weights(wp[n] + rb + at);
       }
-      x[u] = __ldg(reinterpret_cast<const uint4*>(xp + at));
-      if (!in || g >= P.T) x[u] = z;
-      if (!in) {
+      x[u] = ld_tokens(xp + at);
+    }
+  };
+  load(k_lo);
+  for (int k0 = k_lo; k0 < k_hi; k0 += U) {
 #pragma unroll
-        for (int n = 0; n < NW; ++n) a[n][u] = b[n][u] = z;
+    for (int u = 0; u < U; ++u) {
+      const bool in = inside(k0 + u);
+      const uint4 xu = in && g < P.T ? x[u] : z;
+#pragma unroll
+      for (int n = 0; n < NW; ++n) {
+        const uint4 au = in ? a[u][n] : z, bu = in ? b[u][n] : z;
+        mma16816(acc[n], au.x, bu.x, au.y, bu.y, xu.x, xu.y);
+        mma16816(acc[n], au.z, bu.z, au.w, bu.w, xu.z, xu.w);
       }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int n = 0; n < NW; ++n) {
-        mma16816(acc[n], a[n][u].x, b[n][u].x, a[n][u].y, b[n][u].y, x[u].x, x[u].y);
-        mma16816(acc[n], a[n][u].z, b[n][u].z, a[n][u].w, b[n][u].w, x[u].z, x[u].w);
-      }
+    load(k0 + U);
   }
 #pragma unroll
   for (int n = 0; n < NW; ++n)
@@ -236,7 +277,7 @@ __global__ void __launch_bounds__(32 * FV_MAXW) k_fused_few(const FusedParams P)
       v += red[w][0][i][l];
       if (GATED) u += red[w][NW - 1][i][l];
     }
-    store_one(P, t, f, finish(P, v, u, GATED, t, f));
+    store_one(P, t, f, finish(P, v, u, GATED, P.act, t, f));
   }
 }
 
@@ -262,8 +303,8 @@ int launch_few(const FusedParams& P, cudaStream_t st) {
 
 // ------------------------------------------------------------ many tokens
 // CTA pairs (tcgen05 cta_group::2) compute tiles of 256 tokens (128 in each
-// CTA's TMEM lanes) by BN weight rows, K in steps of 64 through a ring of TMA
-// stages.  Of a step each CTA fetches its 128 tokens and half of the BN
+// CTA's TMEM lanes) by BN weight rows, K in steps of 128 (two boxes of 64) through a
+// ring of TMA stages.  Of a step each CTA fetches its 128 tokens and half of the BN
 // weight rows; in the gated product the even CTA's half are rows of w_gate and
 // the odd CTA's the same rows of w_up, so that a tile's columns j and j + BN/2
 // are the gate and the up value of one feature, in one thread.
@@ -286,24 +327,16 @@ constexpr int DN_STAGING = 8 * 4096;  // 4 KB per epilogue warp
 constexpr uint64_t kDrainNs = 200000;
 
 struct DenseParams {
-  CUtensorMap x_map;        // x [T][K], box 64 x 128
+  CUtensorMap x_map;        // x [T][K], box 64 x x_rows
   CUtensorMap w_map, w2_map;  // weights [F][K], box 64 x BN/2
   CUtensorMap y_map;        // y [T][F], box 128 bytes x 32 rows (when tma_y)
   FusedParams f;
   int n_m, n_n, KB, S;
+  int x_rows;               // token rows a CTA fetches: 128, fewer when T has fewer
   int tma_y;
   int vec_r;                // residual rows in 16-byte loads
   int32_t* err;
 };
-
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t a) {
-  float4 r;
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-               : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w)
-               : "r"(a)
-               : "memory");
-  return r;
-}
 
 // Tile order: eight token tiles side by side, then along the features, so that
 // the pairs at work share weight rows and token rows in L2.
@@ -315,36 +348,46 @@ __device__ __forceinline__ void tile_at(const DenseParams& P, int tile, int& m, 
   n = in / rows;
 }
 
-template <int BN, bool GATED>
+// ACT is a template argument: with a switch over the activations in the epilogue its
+// instructions did not stay in the instruction cache (1400 cycles per 1024 values).
+template <int BN, bool GATED, int ACT>
 __global__ void __launch_bounds__(DN_THREADS, 1) k_dense(const __grid_constant__ DenseParams P) {
   constexpr int FT = GATED ? BN / 2 : BN;  // features of a tile
   constexpr int B_BYTES = BN / 2 * 128;
-  constexpr int STAGE = DN_A_BYTES + B_BYTES;
+  constexpr int HALF = DN_A_BYTES + B_BYTES;  // 64 of K
+  constexpr int STAGE = 2 * HALF;
   constexpr int NST = (DN_SMEM - 2048 - DN_STAGING) / STAGE < DN_MAXST
                           ? (DN_SMEM - 2048 - DN_STAGING) / STAGE
                           : DN_MAXST;
-  static_assert(NST * STAGE >= 128 * BN * 4, "a share's sums fit in the stages");
+  static_assert(NST * STAGE + DN_STAGING >= 128 * BN * 4 + 3 * 32 * BN * 4 && BN <= 256,
+                "a share's sums and the other shares' rows fit in front of the barriers");
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   struct Bars {
-    uint64_t full[NST], empty[NST], tfull[2], tempty[2], done;
+    uint64_t full[NST], empty[NST], tfull[2], tempty[2], done, got;
     uint32_t tmem_base;
     volatile int failed;
   };
   unsigned char* staging = base + NST * STAGE;
   Bars& B = *reinterpret_cast<Bars*>(staging + DN_STAGING);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t crank = tc::cluster_rank();
-  const uint32_t lead = crank & ~1u, peer = crank ^ 1u;
+  const uint32_t lead = crank & ~1u;
   const int rank = crank & 1, share = crank >> 1;
   const int n_tiles = P.n_m * P.n_n;
   const int n_clusters = gridDim.x / (2 * P.S), cluster = blockIdx.x / (2 * P.S);
   const int kb0 = P.KB * share / P.S, kb1 = P.KB * (share + 1) / P.S;
 
+  if (threadIdx.x == 32 * 8) {
+    // launch arguments: no earlier kernel writes them
+    tc::prefetch_map(&P.x_map);
+    tc::prefetch_map(&P.w_map);
+    if (GATED) tc::prefetch_map(&P.w2_map);
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < NST; ++s) {
-      mbar_init(&B.full[s], 2);   // each CTA's arrival with its byte count
+      mbar_init(&B.full[s], 1);   // the even CTA's arrival with both CTAs' byte count
       mbar_init(&B.empty[s], 1);  // the MMAs that read the stage have completed
     }
     for (int b = 0; b < 2; ++b) {
@@ -352,6 +395,7 @@ __global__ void __launch_bounds__(DN_THREADS, 1) k_dense(const __grid_constant__
       mbar_init(&B.tempty[b], 16);  // the epilogue warps of both CTAs
     }
     mbar_init(&B.done, 1);
+    mbar_init(&B.got, 1);
     B.failed = 0;
     fence_mbar_init();
   }
@@ -365,32 +409,51 @@ __global__ void __launch_bounds__(DN_THREADS, 1) k_dense(const __grid_constant__
   const uint32_t tmem = B.tmem_base;
 
   if (warp == 8) {
-    if (lane == 0) {
-      int step = 0;
+    if (tc::elect_one()) {
+      int s = 0;
+      uint32_t phase = 1;
       const CUtensorMap* wm = GATED && rank ? &P.w2_map : &P.w_map;
-      for (int tile = cluster; tile < n_tiles && !B.failed; tile += n_clusters) {
+      const uint32_t full = tc::map_to_rank(&B.full[0], lead);
+      bool ok = true;
+      for (int tile = cluster; tile < n_tiles && ok && !B.failed; tile += n_clusters) {
         int m, n;
         tile_at(P, tile, m, n);
         const int t0 = 256 * m + 128 * rank;
         const int f0 = FT * n + (GATED ? 0 : BN / 2 * rank);
-        for (int kb = kb0; kb < kb1; ++kb, ++step) {
-          const int s = step % NST;
-          if (!mbar_wait(&B.empty[s], ((step / NST) & 1) ^ 1, P.err)) {
-            B.failed = 1;
-            break;
-          }
+        // lanes whose tokens are not fetched hold what the stage held before: a lane's
+        // sums are its own token's alone, and nothing past T is stored
+        const bool some = t0 < P.f.T;
+        // what both CTAs' copies of 64 of K bring; the even CTA's barrier counts them
+        // all, and its own thread announces them
+        const uint32_t bytes =
+            2 * B_BYTES + 128u * P.x_rows * (256 * m + 128 < P.f.T ? 2u : 1u);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          ok = mbar_wait(&B.empty[s], phase, P.err);
+          if (!ok) break;
           unsigned char* st = base + (size_t)s * STAGE;
-          const uint32_t fb = tc::map_to_rank(&B.full[s], lead);
-          tc::mbar_arrive_expect_tx_cluster(fb, STAGE);
-          tc::tma_load_2d_pair(st + DN_A_BYTES, wm, 64 * kb, f0, fb);
-          tc::tma_load_2d_pair(st, &P.x_map, 64 * kb, t0, fb);
+          const uint32_t fb = full + 8 * s;
+          const bool two = 128 * kb + 64 < P.f.K;
+          if (rank == 0) mbar_arrive_expect_tx(&B.full[s], two ? 2 * bytes : bytes);
+          tc::tma_load_2d_pair(st + DN_A_BYTES, wm, 128 * kb, f0, fb);
+          if (some) tc::tma_load_2d_pair(st, &P.x_map, 128 * kb, t0, fb);
+          if (two) {
+            tc::tma_load_2d_pair(st + HALF + DN_A_BYTES, wm, 128 * kb + 64, f0, fb);
+            if (some) tc::tma_load_2d_pair(st + HALF, &P.x_map, 128 * kb + 64, t0, fb);
+          }
+          if (++s == NST) s = 0, phase ^= 1;
         }
       }
+      if (!ok) B.failed = 1;
     }
+    __syncwarp();
   } else if (warp == 9) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && tc::elect_one()) {
       constexpr uint32_t id = tc::idesc_bf16(256, BN, false, false);
-      int step = 0, it = 0;
+      const uint16_t both = (uint16_t)(3u << lead);
+      const uint64_t a_desc = tc::desc_sw128(smem_u32(base), 16, 1024);
+      const uint64_t b_desc = tc::desc_sw128(smem_u32(base) + DN_A_BYTES, 16, 1024);
+      int s = 0, it = 0;
+      uint32_t phase = 0;
       bool ok = true;
       for (int tile = cluster; tile < n_tiles && ok && !B.failed; tile += n_clusters, ++it) {
         const int b = it & 1;
@@ -398,28 +461,34 @@ __global__ void __launch_bounds__(DN_THREADS, 1) k_dense(const __grid_constant__
         if (!ok) break;
         tc::fence_after_sync();
         const uint32_t d = tmem + BN * b;
-        for (int kb = kb0; kb < kb1; ++kb, ++step) {
-          const int s = step % NST;
-          ok = mbar_wait(&B.full[s], (step / NST) & 1, P.err);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          ok = mbar_wait(&B.full[s], phase, P.err);
           if (!ok) break;
           tc::fence_after_sync();
-          const uint32_t a0 = smem_u32(base + (size_t)s * STAGE), b0 = a0 + DN_A_BYTES;
+          // descriptors count 16-byte units: a stage, a half of it, 32 bytes (16 of K) a
+          // product
+          const uint64_t at = (uint64_t)(s * (STAGE / 16));
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc::mma_pair_bf16_ss(d, tc::desc_sw128(a0 + 32 * kk, 16, 1024),
-                                 tc::desc_sw128(b0 + 32 * kk, 16, 1024), id,
-                                 (kb > kb0 || kk > 0) ? 1u : 0u);
-          tc::commit_pair(tc::map_to_rank(&B.empty[s], crank));
-          tc::commit_pair(tc::map_to_rank(&B.empty[s], peer));
+            tc::mma_pair_bf16(d, a_desc + at + 2 * kk, b_desc + at + 2 * kk, id,
+                              (kb > kb0 || kk > 0) ? 1u : 0u);
+          if (128 * kb + 64 < P.f.K) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc::mma_pair_bf16(d, a_desc + at + HALF / 16 + 2 * kk,
+                                b_desc + at + HALF / 16 + 2 * kk, id, 1u);
+          }
+          tc::commit_pair_to(&B.empty[s], both);
+          if (++s == NST) s = 0, phase ^= 1;
         }
         if (!ok) break;
-        tc::commit_pair(tc::map_to_rank(&B.tfull[b], crank));
-        tc::commit_pair(tc::map_to_rank(&B.tfull[b], peer));
+        tc::commit_pair_to(&B.tfull[b], both);
       }
       if (!ok) B.failed = 1;
       tc::commit_pair(tc::map_to_rank(&B.done, crank));
       mbar_wait(&B.done, 0, P.err);  // nothing of the pair's is on the tensor cores at exit
     }
+    __syncwarp();
   } else {
     const int quad = warp & 3, half = warp >> 2;
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
@@ -449,12 +518,12 @@ __global__ void __launch_bounds__(DN_THREADS, 1) k_dense(const __grid_constant__
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
           if constexpr (GATED) {
-            activate32(v, P.f.act);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] *= __uint_as_float(u[i]);
+            for (int i = 0; i < 32; ++i) v[i] = activate(v[i], ACT) * __uint_as_float(u[i]);
           } else {
             add_bias32(v, P.f, f);
-            activate32(v, P.f.act);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = activate(v[i], ACT);
             if (t < P.f.T) add_residual32(v, P.f, P.vec_r, t, f);
           }
           // the block into the warp's staging rows of 128 bytes (chunk c of row l
@@ -526,38 +595,66 @@ __global__ void __launch_bounds__(DN_THREADS, 1) k_dense(const __grid_constant__
     }
   }
   if (P.S > 1) {
-    tc::cluster_sync();  // every share's sums are in place
+    // share p finishes rows [rows p / S, rows (p + 1) / S) of its CTA's tokens: every
+    // other share's sums of these rows come here in one bulk copy each
+    tc::fence_async_smem();
+    tc::cluster_sync();  // every CTA of the cluster is past its products
     int m, n;
     tile_at(P, cluster, m, n);
     const int t0 = 256 * m + 128 * rank;
-    const int rows = min(128, P.f.T - t0);
-    if (threadIdx.x < DN_EPI && rows > 0 && !B.failed) {
-      const uint32_t mine = smem_u32(base);
-      uint32_t at[4];
-      for (int p = 0; p < 4; ++p)
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                     : "=r"(at[p])
-                     : "r"(mine), "r"(2 * min(p, P.S - 1) + rank));
-      constexpr int GR = FT / 4;  // groups of four features in a row
-      for (int i = share * DN_EPI + threadIdx.x; i < rows * GR; i += P.S * DN_EPI) {
-        const int row = i / GR, c = i % GR;
-        const int f = FT * n + 4 * c;
-        if (f >= P.f.F) continue;
-        float v[4] = {}, u[4] = {};
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          if (p >= P.S) break;
-          const float4 a = ld_cluster_f4(at[p] + 4 * (BN * row + 4 * (c ^ (row & 7))));
-          v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
-          if (GATED) {
-            const float4 b = ld_cluster_f4(at[p] + 4 * (BN * row + 4 * ((GR + c) ^ (row & 7))));
-            u[0] += b.x, u[1] += b.y, u[2] += b.z, u[3] += b.w;
-          }
-        }
+    const int rows = max(0, min(128, P.f.T - t0));
+    const int r0 = rows * share / P.S, r1 = rows * (share + 1) / P.S;
+    const int slot = (rows + P.S - 1) / P.S * BN;  // floats of one share's rows
+    const float* sums = reinterpret_cast<const float*>(base);
+    const float* others = sums + 128 * BN;
+    if (threadIdx.x == 0) {
+      mbar_arrive_expect_tx(&B.got, (uint32_t)((P.S - 1) * (r1 - r0) * BN * 4));
+      for (int p = 0; p < P.S; ++p) {
+        const int q0 = rows * p / P.S, q1 = rows * (p + 1) / P.S;
+        if (p == share || q0 == q1) continue;
+        const uint32_t to = tc::map_to_rank(others + (size_t)slot * (share - (share > p)),
+                                            2 * p + rank);
+        tc::bulk_s2peer(to, sums + (size_t)BN * q0, (uint32_t)((q1 - q0) * BN * 4),
+                        tc::map_to_rank(&B.got, 2 * p + rank));
+      }
+    }
+    if (threadIdx.x < DN_EPI && !mbar_wait(&B.got, 0, P.err)) B.failed = 1;
+    if (threadIdx.x < DN_EPI && !B.failed) {
+      // a thread keeps its four features and walks down the rows
+      constexpr int GR = FT / 4;
+      static_assert(DN_EPI % GR == 0, "");
+      const int c = threadIdx.x % GR, f = FT * n + 4 * c;
+      float bias[4] = {};
+      if (P.f.bias)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (f + j < P.f.F)
-            store_one(P.f, t0 + row, f + j, finish(P.f, v[j], u[j], GATED, t0 + row, f + j));
+          if (f + j < P.f.F) bias[j] = bf1(P.f.bias[f + j]);
+      const float* from[4];
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+        from[p] = p == share || p >= P.S ? sums + BN * r0
+                                         : others + (size_t)slot * (p - (p > share));
+      const int S = P.S;
+      if (f < P.f.F) {
+#pragma unroll 2
+        for (int r = threadIdx.x / GR; r < r1 - r0; r += DN_EPI / GR) {
+          const int x = (r0 + r) & 7;
+          const int at = BN * r + 4 * (c ^ x), at_u = BN * r + 4 * ((GR + c) ^ x);
+          float v[4] = {bias[0], bias[1], bias[2], bias[3]}, u[4] = {};
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            if (p >= S) break;
+            const float4 a = *reinterpret_cast<const float4*>(from[p] + at);
+            v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+            if (GATED) {
+              const float4 b = *reinterpret_cast<const float4*>(from[p] + at_u);
+              u[0] += b.x, u[1] += b.y, u[2] += b.z, u[3] += b.w;
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = activate(v[j], ACT) * (GATED ? u[j] : 1.f);
+          finish_four(P.f, t0 + r0 + r, f, v);
+        }
       }
     }
   }
@@ -576,28 +673,91 @@ __global__ void __launch_bounds__(DN_THREADS, 1) k_dense(const __grid_constant__
   }
 }
 
+using DenseKernel = void (*)(const DenseParams);
+// [gated 256, 256, 128][activation]
+const DenseKernel kDense[3][4] = {
+    {k_dense<256, true, 0>, k_dense<256, true, 1>, k_dense<256, true, 2>, k_dense<256, true, 3>},
+    {k_dense<256, false, 0>, k_dense<256, false, 1>, k_dense<256, false, 2>,
+     k_dense<256, false, 3>},
+    {k_dense<128, false, 0>, k_dense<128, false, 1>, k_dense<128, false, 2>,
+     k_dense<128, false, 3>}};
+
+// What a device holds at once: clusters of S pairs (they stay inside a GPC).
+struct Room {
+  int clusters[5];
+};
+std::mutex g_attr_mu;
+bool g_attr_done[64] = {false};
+Room g_room[64];
+
+cudaLaunchConfig_t dense_config(cudaLaunchAttribute (&attr)[2], int clusters, int S,
+                                cudaStream_t st) {
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2 * S;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(clusters * 2 * S);
+  cfg.blockDim = dim3(DN_THREADS);
+  cfg.dynamicSmemBytes = DN_SMEM;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cfg;
+}
+
+int dense_attributes(Room& room) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return ER_ECUDA;
+  std::lock_guard<std::mutex> lock(g_attr_mu);
+  if (g_attr_done[dev]) {
+    room = g_room[dev];
+    return ER_OK;
+  }
+  for (auto& row : kDense)
+    for (DenseKernel fn : row)
+      if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, DN_SMEM) !=
+          cudaSuccess)
+        return ER_ECUDA;
+  for (int S = 1; S <= 4; ++S) {
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = dense_config(attr, 1, S, nullptr);
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&g_room[dev].clusters[S], kDense[1][0], &cfg) !=
+        cudaSuccess)
+      return ER_ECUDA;
+  }
+  if (g_room[dev].clusters[1] < 1) return ER_ECUDA;
+  room = g_room[dev];
+  g_attr_done[dev] = true;
+  return ER_OK;
+}
+
 struct DensePlan {
   int BN, S, clusters;
 };
 
 // The tile width and the shares of K, by the estimated cycles of a pair.  A K step
-// costs the longer of its MMAs (2 BN cycles) and its fetches (one SM takes about
-// 65 bytes per cycle from L2, about 24 of them when they come from HBM).
-DensePlan choose_plan(int T, int F, int K, bool gated) {
-  const int pairs = num_sms() / 2, KB = (K + 63) / 64, n_m = (T + 255) / 256;
+// costs the longer of its MMAs (4 BN cycles) and its fetches (measured: one SM's TMA
+// brings about 60 bytes per cycle in these boxes); joining shares costs the copies
+// between the CTAs (measured: 16 bytes per cycle into a CTA) and two more barriers of
+// the cluster.
+DensePlan choose_plan(int T, int F, int K, bool gated, const Room& room) {
+  const int KB = (K + 127) / 128, n_m = (T + 255) / 256, rows = T < 128 ? T : 128;
   DensePlan best{256, 1, 1};
   double least = 1e300;
   for (int BN : {256, 128}) {
     if (gated && BN != 256) continue;
     const int FT = gated ? BN / 2 : BN, tiles = n_m * ((F + FT - 1) / FT);
     for (int S = 1; S <= 4 && S <= KB; ++S) {
-      if (S > 1 && tiles * S > pairs) break;
-      const double mma = 2.0 * BN, fetch = (DN_A_BYTES + 64.0 * BN) / 65.0;
-      const double hbm = n_m == 1 ? 64.0 * BN / 24.0 : 0.0;
-      const double step = mma > fetch ? (mma > hbm ? mma : hbm) : (fetch > hbm ? fetch : hbm);
-      const int clusters = S > 1 ? tiles : (tiles < pairs ? tiles : pairs);
+      if (S > 1 && tiles > room.clusters[S]) break;
+      const double mma = 4.0 * BN, fetch = (256.0 * rows + 128.0 * BN) / 60.0;
+      const int clusters = tiles < room.clusters[S] ? tiles : room.clusters[S];
       const int waves = (tiles + clusters - 1) / clusters;
-      const double cost = waves * ((KB + S - 1) / S) * step + (S > 1 ? 3000.0 : 1500.0);
+      const double join = 4000.0 + 4.0 * BN * rows * (S - 1) / S / 16.0;
+      const double cost =
+          waves * ((KB + S - 1) / S) * (mma > fetch ? mma : fetch) + (S > 1 ? join : 1500.0);
       if (cost < least) {
         least = cost;
         best = DensePlan{BN, S, clusters};
@@ -607,60 +767,35 @@ DensePlan choose_plan(int T, int F, int K, bool gated) {
   return best;
 }
 
-std::mutex g_attr_mu;
-bool g_attr_done[64] = {false};
-
-int dense_attributes() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return ER_ECUDA;
-  std::lock_guard<std::mutex> lock(g_attr_mu);
-  if (g_attr_done[dev]) return ER_OK;
-  for (auto* fn : {k_dense<256, false>, k_dense<128, false>, k_dense<256, true>})
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, DN_SMEM) !=
-        cudaSuccess)
-      return ER_ECUDA;
-  g_attr_done[dev] = true;
-  return ER_OK;
-}
 
 int launch_dense(const FusedParams& F, int32_t* err, cudaStream_t st) {
   const bool gated = F.w2 != nullptr;
-  const DensePlan plan = choose_plan(F.T, F.F, F.K, gated);
+  Room room;
+  const int rc = dense_attributes(room);
+  if (rc != ER_OK) return rc;
+  const DensePlan plan = choose_plan(F.T, F.F, F.K, gated, room);
   DenseParams P{};
   P.f = F;
   const int FT = gated ? plan.BN / 2 : plan.BN;
   P.n_m = (F.T + 255) / 256;
   P.n_n = (F.F + FT - 1) / FT;
-  P.KB = (F.K + 63) / 64;
+  P.KB = (F.K + 127) / 128;
   P.S = plan.S;
   P.err = err;
   const int el = F.f32 ? 4 : 2;
   // a TMA store rounds a clipped row up to 16 bytes
   P.tma_y = plan.S == 1 && aligned16(F.y) && F.ldy * el % 16 == 0 && F.F * el % 16 == 0;
   P.vec_r = aligned16(F.residual) && F.ldr * el % 16 == 0;
-  if (!encode_rows(&P.x_map, F.x, false, F.K, F.T, F.ldx * 2, 64, 128) ||
+  P.x_rows = F.T >= 128 ? 128 : (F.T + 7) / 8 * 8;
+  if (!encode_rows(&P.x_map, F.x, false, F.K, F.T, F.ldx * 2, 64, P.x_rows) ||
       !encode_rows(&P.w_map, F.w, false, F.K, F.F, (uint64_t)F.K * 2, 64, plan.BN / 2) ||
       (gated && !encode_rows(&P.w2_map, F.w2, false, F.K, F.F, (uint64_t)F.K * 2, 64, plan.BN / 2)) ||
       (P.tma_y && !encode_rows(&P.y_map, F.y, F.f32, F.F, F.T, F.ldy * el, 128 / el, 32)))
     return ER_ECUDA;
-  const int rc = dense_attributes();
-  if (rc != ER_OK) return rc;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2 * plan.S;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(plan.clusters * 2 * plan.S);
-  cfg.blockDim = dim3(DN_THREADS);
-  cfg.dynamicSmemBytes = DN_SMEM;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  const cudaError_t e = gated ? cudaLaunchKernelEx(&cfg, k_dense<256, true>, P)
-                        : plan.BN == 256 ? cudaLaunchKernelEx(&cfg, k_dense<256, false>, P)
-                                         : cudaLaunchKernelEx(&cfg, k_dense<128, false>, P);
+  const cudaLaunchConfig_t cfg = dense_config(attr, plan.clusters, plan.S, st);
+  const cudaError_t e =
+      cudaLaunchKernelEx(&cfg, kDense[gated ? 0 : plan.BN == 256 ? 1 : 2][F.act], P);
   if (e != cudaSuccess) return ER_ECUDA;
   count_launches(1);
   return launch_status();

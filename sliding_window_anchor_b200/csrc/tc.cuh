@@ -155,6 +155,10 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // One 4-D box (x innermost, elements; 16-byte multiple).
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z,
                                             int w, uint64_t* bar) {
@@ -213,6 +217,36 @@ __device__ __forceinline__ void mma_pair_bf16_ss(uint32_t d_tmem, uint64_t a, ui
       "r"(0u), "r"(0u), "r"(0u));
 }
 
+// True in one lane of a converged warp.  Code of tcgen05 and TMA instructions takes its
+// operands from uniform registers: behind this predicate they are issued as they stand,
+// behind a test of the lane number the compiler loops over the lanes that might be active.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(p));
+  return p != 0;
+}
+
+// mma_pair_bf16_ss without the (empty) mask of lanes.
+__device__ __forceinline__ void mma_pair_bf16(uint32_t d_tmem, uint64_t a, uint64_t b,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// One arrival on the mbarrier `bar` (the same offset) of every CTA of the cluster in
+// `mask`, once every pair MMA issued so far by this thread has completed.
+__device__ __forceinline__ void commit_pair_to(uint64_t* bar, uint16_t mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(smem_u32(bar)),
+      "h"(mask)
+      : "memory");
+}
+
 __device__ __forceinline__ void mma_pair_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
                                                  uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -268,6 +302,18 @@ __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t by
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
                "r"(smem_u32(src)), "r"(bytes)
                : "memory");
+}
+
+// A bulk copy of `bytes` (multiple of 16) from this CTA's shared memory to the
+// shared::cluster address `dst` of a CTA of the cluster, counted on the mbarrier at
+// shared::cluster address `bar` of that CTA.
+__device__ __forceinline__ void bulk_s2peer(uint32_t dst, const void* src, uint32_t bytes,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "r"(smem_u32(src)), "r"(bytes), "r"(bar)
+      : "memory");
 }
 
 __device__ __forceinline__ void bulk_commit() {
