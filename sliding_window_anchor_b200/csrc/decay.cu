@@ -7,7 +7,10 @@
 //
 // per value head, S FP32 [k_dim][v_dim]; value head h reads the q and k of head
 // h / (v_heads / k_heads).
+#include <mutex>
+
 #include "common.cuh"
+#include "tc.cuh"
 
 namespace er {
 namespace {
@@ -45,49 +48,767 @@ __device__ __forceinline__ bool sequence_rows(const DecayParams& P, int b, int& 
   return true;
 }
 
-// One block per (32 columns of a value head's state, sequence), token by token;
-// thread (r, c) holds rows r, r + 4, ... of column c.
-template <int DK>
-__global__ void __launch_bounds__(128) k_decay_tokens(const DecayParams P) {
-  __shared__ float qs[DK], ks[DK], part[4][32];
-  const int b = blockIdx.y, slices = P.DV / 32;
-  const int h = blockIdx.x / slices, c0 = 32 * (blockIdx.x % slices);
-  const int hk = h / (P.HV / P.HK);
-  const int c = threadIdx.x & 31, r = threadIdx.x >> 5;
-  int row, begin, end;
-  if (!sequence_rows(P, b, row, begin, end)) return;
-  float* S = P.state + (((size_t)row * P.HV + h) * DK) * P.DV + c0 + c;
-  float s[DK / 4];
-  for (int i = 0; i < DK / 4; ++i) s[i] = S[(size_t)(r + 4 * i) * P.DV];
-  for (int t = begin; t < end; ++t) {
-    for (int i = threadIdx.x; i < DK; i += 128) {
-      qs[i] = bf1(P.q[t * P.ldq + hk * DK + i]);
-      ks[i] = bf1(P.k[t * P.ldk + hk * DK + i]);
-    }
-    const float a = expf(P.g[t * P.ldg + h]);
-    const float v = bf1(P.v[t * P.ldv + h * P.DV + c0 + c]);
-    __syncthreads();
-    float o = 0.f;
-    for (int i = 0; i < DK / 4; ++i) {
-      s[i] = fmaf(s[i], a, ks[r + 4 * i] * v);
-      o = fmaf(qs[r + 4 * i], s[i], o);
-    }
-    part[r][c] = o;
-    __syncthreads();
-    if (r == 0)
-      P.o[t * P.ldo + h * P.DV + c0 + c] =
-          f2bf(P.scale * (part[0][c] + part[1][c] + part[2][c] + part[3][c]));
+// ------------------------------------------------------------ single tokens
+// One block per (sequence, value head, COLS columns of its state): the state streams
+// through registers once, 16 bytes a thread and row; every thread's rows are
+// requested before the first is used.  o's sums over the rows are joined in a fixed
+// order.
+constexpr int DD_THREADS = 256;
+
+template <int DK, int COLS>
+__global__ void __launch_bounds__(DD_THREADS) k_decay_decode(const DecayParams P) {
+  constexpr int LN = COLS / 4;         // threads of a row
+  constexpr int RP = DD_THREADS / LN;  // rows of a pass
+  constexpr int N = DK / RP;           // rows of a thread
+  static_assert(N >= 1, "");
+  __shared__ float qs[DK], ks[DK];
+  __shared__ float4 part[DD_THREADS / 32][LN];
+  grid_dep_wait();
+  grid_dep_trigger();
+  const int slices = P.DV / COLS;
+  const int unit = blockIdx.x / slices, c0 = COLS * (blockIdx.x % slices);
+  const int b = unit / P.HV, h = unit % P.HV, hk = h / (P.HV / P.HK);
+  const int c = threadIdx.x % LN, r = threadIdx.x / LN;
+  for (int i = threadIdx.x; i < DK; i += DD_THREADS) {
+    qs[i] = bf1(P.q[b * P.ldq + hk * DK + i]);
+    ks[i] = bf1(P.k[b * P.ldk + hk * DK + i]);
   }
-  for (int i = 0; i < DK / 4; ++i) S[(size_t)(r + 4 * i) * P.DV] = s[i];
+  int row, begin, end;
+  if (!sequence_rows(P, b, row, begin, end)) return;  // holds the block's barrier
+  float* S = P.state + (((size_t)row * P.HV + h) * DK + r) * P.DV + c0 + 4 * c;
+  float4 s[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    s[i] = *reinterpret_cast<const float4*>(S + (size_t)(RP * i) * P.DV);
+  const float a = expf(P.g[b * P.ldg + h]);
+  const uint2 vw = *reinterpret_cast<const uint2*>(P.v + b * P.ldv + h * P.DV + c0 + 4 * c);
+  const float4 v = make_float4(bf_lo(vw.x), bf_hi(vw.x), bf_lo(vw.y), bf_hi(vw.y));
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float k = ks[r + RP * i], q = qs[r + RP * i];
+    s[i].x = fmaf(s[i].x, a, k * v.x), o.x = fmaf(q, s[i].x, o.x);
+    s[i].y = fmaf(s[i].y, a, k * v.y), o.y = fmaf(q, s[i].y, o.y);
+    s[i].z = fmaf(s[i].z, a, k * v.z), o.z = fmaf(q, s[i].z, o.z);
+    s[i].w = fmaf(s[i].w, a, k * v.w), o.w = fmaf(q, s[i].w, o.w);
+    *reinterpret_cast<float4*>(S + (size_t)(RP * i) * P.DV) = s[i];
+  }
+#pragma unroll
+  for (int m = LN; m < 32; m <<= 1) {
+    o.x += __shfl_xor_sync(0xffffffffu, o.x, m), o.y += __shfl_xor_sync(0xffffffffu, o.y, m);
+    o.z += __shfl_xor_sync(0xffffffffu, o.z, m), o.w += __shfl_xor_sync(0xffffffffu, o.w, m);
+  }
+  if ((threadIdx.x & 31) < LN) part[threadIdx.x >> 5][threadIdx.x & 31] = o;
+  __syncthreads();
+  if (threadIdx.x < LN) {
+    o = part[0][threadIdx.x];
+#pragma unroll
+    for (int w = 1; w < DD_THREADS / 32; ++w) {
+      const float4 x = part[w][threadIdx.x];
+      o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
+    }
+    *reinterpret_cast<uint2*>(P.o + b * P.ldo + h * P.DV + c0 + 4 * threadIdx.x) =
+        make_uint2(pack_bf2(P.scale * o.x, P.scale * o.y), pack_bf2(P.scale * o.z, P.scale * o.w));
+  }
 }
 
-int launch_tokens(const DecayParams& P, cudaStream_t st) {
-  const dim3 grid(P.HV * P.DV / 32, P.B);
-  if (P.DK == 64)
-    k_decay_tokens<64><<<grid, 128, 0, st>>>(P);
-  else
-    k_decay_tokens<128><<<grid, 128, 0, st>>>(P);
+int launch_pdl(void (*fn)(const DecayParams), int blocks, int threads, const DecayParams& P,
+               cudaStream_t st) {
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, fn, P) != cudaSuccess) return ER_ECUDA;
   count_launches(1);
+  return launch_status();
+}
+
+int launch_decode(const DecayParams& P, cudaStream_t st) {
+  // whole rows of the state where they give every SM two blocks, else narrower ones
+  const int units = P.B * P.HV;
+  const bool wide = units >= 2 * num_sms();
+  const int cols = wide ? P.DV : 32;
+  const int blocks = units * (P.DV / cols);
+  if (P.DK == 64)
+    return launch_pdl(cols == 128  ? k_decay_decode<64, 128>
+                      : cols == 64 ? k_decay_decode<64, 64>
+                                   : k_decay_decode<64, 32>,
+                      blocks, DD_THREADS, P, st);
+  return launch_pdl(cols == 128  ? k_decay_decode<128, 128>
+                    : cols == 64 ? k_decay_decode<128, 64>
+                                 : k_decay_decode<128, 32>,
+                    blocks, DD_THREADS, P, st);
+}
+
+// ------------------------------------------------------------ prompts
+// A sequence is walked in chunks of 128 tokens.  With G_i the sum of the log-decays of
+// a chunk's tokens 0..i and S the state in front of it:
+//   o_i = scale · (e^{G_i} Sᵀ q_i + Σ_{j<=i} (q_i·k_j) e^{G_i - G_j} v_j)
+//   S  <- e^{G_127} S + Σ_j k_j (e^{G_127 - G_j} v_j)ᵀ
+// as four tensor-core products (tcgen05): Q Kᵀ (masked and decayed in registers, back
+// into TMEM as BF16), that times V, Q S (S as BF16), Kᵀ Ṽ.  The state's product is
+// exact to 2^-16: its decayed values Ṽ go in as two BF16 terms, hi + lo; the
+// state itself stays in FP32 in TMEM, where the chunk's decay is applied to it.  Of
+// o's terms each meets one rounding to BF16 (2^-8), like its result.  G is summed in
+// FP64 and kept as two floats, so that differences are exact however large G is.
+//
+// A CTA walks 64 columns of one value head through one segment of a sequence.
+// Long sequences are cut into segments of L tokens that are walked at the same time:
+// a first launch (STATES) finds what each segment's own tokens leave behind, and a
+// segment's walk starts from those of the segments in front of it.  There a
+// segment's chunks are walked from its end, so that all decays are known and no
+// product waits for another.
+//
+// Warps: 0 — TMA; 1 — the products; 2 — decays; 4-11 — Q Kᵀ's rows; 12-15 — Ṽ and o;
+// 16-19 — the state.  Non-finite values of v are kept out of the products of the
+// tokens in front of them: they enter V as zero, the state as NaN, and o's column is
+// NaN from that token on.
+constexpr int CH = 128;
+constexpr int DC_THREADS = 640;
+constexpr uint64_t kDrainNs = 200000;
+
+struct ChunkParams {
+  CUtensorMap q_map, k_map, v_map;  // rows of [T][heads · dim], boxes 64 x 128
+  DecayParams d;
+  int L;        // tokens of a segment (a multiple of CH)
+  float* W;     // [slots][HV][DK][DV] what a segment leaves, for sequences of two and more
+  double* Wg;   // [slots][HV] a segment's log2 decay
+};
+
+struct alignas(16) Gates {
+  float hi[CH], lo[CH];  // G in log2 units, hi + lo
+  float w[CH];           // e^{G_end - G_j}; 0 behind the sequence
+  float e[CH];           // scale · e^{G_i}
+  float tot;
+};
+
+struct Item {
+  int found, row, b, seg, nseg, slot, t0, t1;
+};
+
+// Segment `index` of the call's sequences, by one warp; reports bad rows.
+__device__ __forceinline__ void find_item(const DecayParams& P, int L, int index, Item* out) {
+  const int lane = threadIdx.x & 31;
+  int acc = 0, slots = 0;
+  long long tokens = 0;
+  Item it{};
+  for (int b0 = 0; b0 < P.B; b0 += 32) {
+    const int b = b0 + lane;
+    int n = 0, begin = 0, end = 0, row = 0;
+    if (b < P.B) {
+      begin = P.cu[b], end = P.cu[b + 1], row = P.seq_ids[b];
+      if (begin < 0 || end < begin || end > P.T || row < 0 || row >= P.s_max) {
+        set_dev_error(P.err, ER_EINVAL);
+        end = begin;
+      }
+    }
+    // together they have T tokens at most: the segments that the grid and the workspace
+    // have room for
+    long long len = tokens + (end - begin);
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, len, m);
+      if (lane >= m) len += x - tokens;
+    }
+    tokens = __shfl_sync(0xffffffffu, len, 31);
+    if (len <= P.T)
+      n = (end - begin + L - 1) / L;
+    else if (end > begin)
+      set_dev_error(P.err, ER_EINVAL);
+    int sum = n, many = n > 1 ? n : 0;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, sum, m), y = __shfl_up_sync(0xffffffffu, many, m);
+      if (lane >= m) sum += x, many += y;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, acc + sum > index);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      if (lane == l) {
+        it.found = 1, it.row = row, it.b = b, it.nseg = n;
+        it.seg = index - (acc + sum - n);
+        it.slot = slots + many - (n > 1 ? n : 0);
+        it.t0 = begin + L * it.seg;
+        it.t1 = min(end, it.t0 + L);
+        *out = it;
+      }
+      return;
+    }
+    acc += __shfl_sync(0xffffffffu, sum, 31);
+    slots += __shfl_sync(0xffffffffu, many, 31);
+  }
+  if (lane == 0) *out = it;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int DK, bool STATES>
+__global__ void __launch_bounds__(DC_THREADS, 1)
+    k_decay_chunks(const __grid_constant__ ChunkParams P) {
+  constexpr int QB = DK * 256;  // bytes of a chunk's q (or k) rows: 64-column blocks of 16 KB
+  constexpr int VB = 16384;
+  constexpr int STAGE = 2 * QB + VB;
+  constexpr uint32_t T_P = 0, T_PT = 128, T_S = 192, T_O = 256;  // TMEM columns
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* base = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  unsigned char* vt = base + 2 * STAGE;  // Ṽ: hi, lo
+  unsigned char* sb = vt + 2 * VB;       // S in BF16, [DK][64]
+  struct Shared {
+    Gates gate[2];
+    int colbad[4][64];  // first token of a chunk with a non-finite v, by column
+    uint64_t full[2], empty[2], gate_full[2], gate_empty[2], o_full[2], o_empty[2];
+    uint64_t p_full, pt_full, pt_empty, vt_full, s_full, sb_full, done;
+    double g_total;
+    Item item;
+    uint32_t tmem_base;
+    volatile int failed;
+  };
+  Shared& B = *reinterpret_cast<Shared*>(sb + DK * 128);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const DecayParams& D = P.d;
+  const int slices = D.DV / 64, per = D.HV * slices;
+  const int h = blockIdx.x % per / slices, c0 = 64 * (blockIdx.x % slices);
+  const int hk = h / (D.HV / D.HK);
+
+  grid_dep_wait();
+  grid_dep_trigger();
+  if (warp == 0) find_item(D, P.L, blockIdx.x / per, &B.item);
+  if (threadIdx.x == 32) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&B.full[i], 1);
+      mbar_init(&B.empty[i], 1);
+      mbar_init(&B.gate_full[i], 1);
+      mbar_init(&B.gate_empty[i], STATES ? 4 : 16);
+      mbar_init(&B.o_full[i], 1);
+      mbar_init(&B.o_empty[i], 4);
+    }
+    mbar_init(&B.p_full, 1);
+    mbar_init(&B.pt_full, 8);
+    mbar_init(&B.pt_empty, 1);
+    mbar_init(&B.vt_full, 4);
+    mbar_init(&B.s_full, 1);
+    mbar_init(&B.sb_full, 4);
+    mbar_init(&B.done, 1);
+    B.failed = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const Item it = B.item;
+  if (!it.found || (STATES && it.nseg < 2)) return;
+  int same = 0;
+  for (int j = threadIdx.x; j < it.b; j += DC_THREADS) same |= D.seq_ids[j] == it.row;
+  if (__syncthreads_or(same)) {
+    if (threadIdx.x == 0) set_dev_error(D.err, ER_EINVAL);
+    return;
+  }
+  if (warp == 1) tc::tmem_alloc(&B.tmem_base, 512);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = B.tmem_base;
+  const int n = (it.t1 - it.t0 + CH - 1) / CH;
+  const size_t plane = (size_t)DK * D.DV;
+  const float* W0 = P.W + ((size_t)it.slot * D.HV + h) * plane;
+
+  // a wait of a whole warp: false (in every lane) when it gave up or another one did
+  auto wait = [&](uint64_t* bar, int phase) {
+    const bool ok = mbar_wait(bar, (uint32_t)phase & 1u, D.err);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    B.failed = 1;
+    return false;
+  };
+  auto arrive = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------- TMA
+    if (tc::elect_one()) {
+      bool ok = true;
+      for (int c = 0; c < n && ok; ++c) {
+        const int s = c & 1, t = it.t0 + CH * (STATES ? n - 1 - c : c);
+        ok = mbar_wait(&B.empty[s], ((c >> 1) & 1) ^ 1, D.err);
+        if (!ok) break;
+        unsigned char* st = base + s * STAGE;
+        mbar_arrive_expect_tx(&B.full[s], STATES ? QB + VB : STAGE);
+#pragma unroll
+        for (int x = 0; x < DK / 64; ++x) {
+          tc::tma_load_2d(st + QB + 16384 * x, &P.k_map, DK * hk + 64 * x, t, &B.full[s]);
+          if (!STATES)
+            tc::tma_load_2d(st + 16384 * x, &P.q_map, DK * hk + 64 * x, t, &B.full[s]);
+        }
+        tc::tma_load_2d(st + 2 * QB, &P.v_map, D.DV * h + c0, t, &B.full[s]);
+      }
+      if (!ok) B.failed = 1;
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // -------------------------------------------------------- products
+    if (tc::elect_one()) {
+      constexpr uint32_t id_p = tc::idesc_bf16(128, 128, false, false);
+      constexpr uint32_t id_o = tc::idesc_bf16(128, 64, false, true);
+      constexpr uint32_t id_s = tc::idesc_bf16(128, 64, true, true);
+      const uint32_t b0 = smem_u32(base), v0 = smem_u32(vt), s0 = smem_u32(sb);
+      bool ok = true;
+      auto scores = [&](int s) {  // Q Kᵀ
+        const uint32_t q = b0 + s * STAGE, k = q + QB;
+#pragma unroll
+        for (int kk = 0; kk < DK / 16; ++kk) {
+          const uint32_t at = 16384 * (kk >> 2) + 32 * (kk & 3);
+          tc::mma_bf16(tmem + T_P, tc::desc_sw128(q + at, 16, 1024),
+                       tc::desc_sw128(k + at, 16, 1024), id_p, kk > 0);
+        }
+        tc::commit(&B.p_full);
+      };
+      for (int c = 0; c < n && ok; ++c) {
+        const int s = c & 1, ph = (c >> 1) & 1;
+        const uint32_t q = b0 + s * STAGE, k = q + QB, v = k + QB;
+        if (!STATES) {
+          if (c == 0) {
+            ok = mbar_wait(&B.full[0], 0, D.err);
+            if (!ok) break;
+            tc::fence_after_sync();
+            scores(0);
+          }
+          // Q S
+          ok = mbar_wait(&B.sb_full, c & 1, D.err) && mbar_wait(&B.o_empty[s], ph ^ 1, D.err);
+          if (!ok) break;
+          tc::fence_after_sync();
+#pragma unroll
+          for (int kk = 0; kk < DK / 16; ++kk)
+            tc::mma_bf16(tmem + T_O + 128 * s,
+                         tc::desc_sw128(q + 16384 * (kk >> 2) + 32 * (kk & 3), 16, 1024),
+                         tc::desc_sw128(s0 + 2048 * kk, 8192, 1024), id_o, kk > 0);
+        } else {
+          ok = mbar_wait(&B.full[s], ph, D.err);
+          if (!ok) break;
+        }
+        // S += Kᵀ Ṽ (with k_dim 64, lanes 64.. take v's rows for columns of k: never read)
+        ok = mbar_wait(&B.vt_full, c & 1, D.err);
+        if (!ok) break;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int kk = 0; kk < CH / 16; ++kk)
+            tc::mma_bf16(tmem + T_S, tc::desc_sw128(k + 2048 * kk, 16384, 1024),
+                         tc::desc_sw128(v0 + VB * part + 2048 * kk, 8192, 1024), id_s,
+                         !STATES || c > 0 || part > 0 || kk > 0);
+        tc::commit(&B.s_full);
+        if (STATES) {
+          tc::commit(&B.empty[s]);
+          continue;
+        }
+        // the masked products times V
+        ok = mbar_wait(&B.pt_full, c & 1, D.err);
+        if (!ok) break;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int kk = 0; kk < CH / 16; ++kk)
+          tc::mma_bf16_a_tmem(tmem + T_O + 128 * s + 64, tmem + T_PT + 8 * kk,
+                              tc::desc_sw128(v + 2048 * kk, 8192, 1024), id_o, kk > 0);
+        tc::commit(&B.o_full[s]);
+        tc::commit(&B.pt_empty);
+        tc::commit(&B.empty[s]);
+        if (c + 1 < n) {
+          ok = mbar_wait(&B.full[s ^ 1], ((c + 1) >> 1) & 1, D.err);
+          if (!ok) break;
+          tc::fence_after_sync();
+          scores(s ^ 1);
+        }
+      }
+      if (!ok) B.failed = 1;
+      tc::commit(&B.done);
+      mbar_wait(&B.done, 0, D.err);  // nothing is on the tensor cores at exit
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ---------------------------------------------------------- decays
+    constexpr double kLog2e = 1.4426950408889634;
+    double R = 0.0;  // STATES: the decay behind the chunk
+    for (int c = 0; c < n; ++c) {
+      const int t = it.t0 + CH * (STATES ? n - 1 - c : c) + 4 * lane;
+      double G[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float g = t + i < it.t1 ? D.g[(t + i) * D.ldg + h] : 0.f;
+        if (g < -1000.f) g = -1000.f;  // e^-1000 is 0, and -inf has no differences
+        G[i] = (double)g * kLog2e + (i ? G[i - 1] : 0.0);
+      }
+      double sum = G[3];
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        const double x = __shfl_up_sync(0xffffffffu, sum, m);
+        if (lane >= m) sum += x;
+      }
+      const double front = sum - G[3], total = __shfl_sync(0xffffffffu, sum, 31);
+      if (!wait(&B.gate_empty[c & 1], ((c >> 1) & 1) ^ 1)) break;
+      Gates& g = B.gate[c & 1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const double x = front + G[i];
+        const float hi = (float)x;
+        g.hi[4 * lane + i] = hi;
+        g.lo[4 * lane + i] = (float)(x - (double)hi);
+        g.w[4 * lane + i] = t + i < it.t1 ? exp2f((float)(R + (total - x))) : 0.f;
+        g.e[4 * lane + i] = D.scale * exp2f(hi);
+      }
+      if (lane == 0) g.tot = exp2f((float)total);
+      if (STATES) {
+        R += total;
+        if (lane == 0) B.g_total = R;
+      }
+      arrive(&B.gate_full[c & 1]);
+    }
+    if (STATES && lane == 0 && c0 == 0) P.Wg[(size_t)(it.slot + it.seg) * D.HV + h] = R;
+  } else if (warp >= 4 && warp < 12) {
+    // ----------------------------------------------- Q Kᵀ's rows, masked
+    if (!STATES) {
+      const int quad = warp & 3, half = (warp - 4) >> 2;
+      const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+      const int i = 32 * quad + lane;
+      // columns right of the diagonal block stay zero
+      uint32_t z[16] = {};
+      for (int cb = half; cb < 4; cb += 2) tc::tmem_st16(tmem + lanes + T_PT + 16 * cb, z);
+      for (int c = 0; c < n; ++c) {
+        if (!wait(&B.p_full, c) || !wait(&B.gate_full[c & 1], c >> 1) ||
+            !wait(&B.pt_empty, c + 1))
+          break;
+        tc::fence_after_sync();
+        const Gates& g = B.gate[c & 1];
+        const float hi = g.hi[i], lo = g.lo[i];
+#pragma unroll 1
+        for (int cb = half; cb <= quad; cb += 2) {
+          uint32_t r[32], o[16];
+          tc::tmem_ld32(tmem + lanes + T_P + 32 * cb, r);
+          tc::tmem_wait_ld();
+          // a column right of the diagonal is masked, whatever it holds
+          const int last = cb == quad ? lane : 31;
+#pragma unroll
+          for (int x = 0; x < 32; x += 4) {
+            const float4 gh = *reinterpret_cast<const float4*>(&g.hi[32 * cb + x]);
+            const float4 gl = *reinterpret_cast<const float4*>(&g.lo[32 * cb + x]);
+            const float p0 = __uint_as_float(r[x]) * ex2((hi - gh.x) + (lo - gl.x));
+            const float p1 = __uint_as_float(r[x + 1]) * ex2((hi - gh.y) + (lo - gl.y));
+            const float p2 = __uint_as_float(r[x + 2]) * ex2((hi - gh.z) + (lo - gl.z));
+            const float p3 = __uint_as_float(r[x + 3]) * ex2((hi - gh.w) + (lo - gl.w));
+            o[x / 2] = pack_bf2(x <= last ? p0 : 0.f, x + 1 <= last ? p1 : 0.f);
+            o[x / 2 + 1] = pack_bf2(x + 2 <= last ? p2 : 0.f, x + 3 <= last ? p3 : 0.f);
+          }
+          tc::tmem_st16(tmem + lanes + T_PT + 16 * cb, o);
+        }
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        arrive(&B.pt_full);
+        if (lane == 0) mbar_arrive(&B.gate_empty[c & 1]);
+      }
+    }
+  } else if (warp >= 12 && warp < 16) {
+    // ------------------------------------------------------- Ṽ, then o
+    const int quad = warp & 3, j = 32 * quad + lane;
+    const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+    float e = 0.f;
+    for (int c = 0; c <= n; ++c) {
+      const float e_prev = e;
+      if (c < n) {
+        const int s = c & 1, t = it.t0 + CH * (STATES ? n - 1 - c : c) + j;
+        if (!STATES && threadIdx.x - 384 < 64) B.colbad[c & 3][threadIdx.x - 384] = CH;
+        named_bar_sync(1, 128);
+        if (!wait(&B.full[s], c >> 1) || !wait(&B.gate_full[s], c >> 1) ||
+            (c > 0 && !wait(&B.s_full, c - 1)))
+          break;
+        const float w = B.gate[s].w[j];
+        e = B.gate[s].e[j];
+        unsigned char* st = base + s * STAGE;
+        unsigned char* v = st + 2 * QB + 128 * j;
+        const int sw = j & 7;
+        if (t < it.t1) {
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            uint4* at = reinterpret_cast<uint4*>(v + 16 * (x ^ sw));
+            const uint4 y = *at;
+            uint32_t in[4] = {y.x, y.y, y.z, y.w}, hi[4], lo[4];
+            bool bad = false;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              const float a = bf_lo(in[m]) * w, b = bf_hi(in[m]) * w;
+              hi[m] = pack_bf2(a, b);
+              lo[m] = pack_bf2(a - bf_lo(hi[m]), b - bf_hi(hi[m]));
+              bad |= (in[m] & 0x7F80u) == 0x7F80u || (in[m] & 0x7F800000u) == 0x7F800000u;
+            }
+            if (bad) {
+#pragma unroll
+              for (int m = 0; m < 4; ++m) {
+                if ((in[m] & 0x7F80u) == 0x7F80u) {
+                  if (!STATES) atomicMin(&B.colbad[c & 3][8 * x + 2 * m], j);
+                  in[m] &= 0xFFFF0000u;
+                  hi[m] |= 0x7FFFu;
+                }
+                if ((in[m] & 0x7F800000u) == 0x7F800000u) {
+                  if (!STATES) atomicMin(&B.colbad[c & 3][8 * x + 2 * m + 1], j);
+                  in[m] &= 0x0000FFFFu;
+                  hi[m] |= 0x7FFF0000u;
+                }
+              }
+              *at = make_uint4(in[0], in[1], in[2], in[3]);
+            }
+            *reinterpret_cast<uint4*>(vt + 128 * j + 16 * (x ^ sw)) =
+                make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(vt + VB + 128 * j + 16 * (x ^ sw)) =
+                make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+        } else {
+          // behind the sequence: another one's rows, or nothing
+          const uint4 z = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            *reinterpret_cast<uint4*>(v + 16 * x) = z;
+            *reinterpret_cast<uint4*>(vt + 128 * j + 16 * x) = z;
+            *reinterpret_cast<uint4*>(vt + VB + 128 * j + 16 * x) = z;
+#pragma unroll
+            for (int y = 0; y < DK / 64; ++y)
+              *reinterpret_cast<uint4*>(st + QB + 16384 * y + 128 * j + 16 * x) = z;
+          }
+        }
+        tc::fence_async_smem();
+        arrive(&B.vt_full);
+        if (lane == 0) mbar_arrive(&B.gate_empty[s]);
+      }
+      if (!STATES && c > 0) {
+        const int cc = c - 1, s = cc & 1, t = it.t0 + CH * cc + j;
+        if (c == n) named_bar_sync(1, 128);  // the last chunk's marks
+        if (!wait(&B.o_full[s], cc >> 1)) break;
+        tc::fence_after_sync();
+        uint16_t* o = D.o + t * D.ldo + h * D.DV + c0;
+#pragma unroll
+        for (int cb = 0; cb < 4; ++cb) {
+          uint32_t a[16], b[16];
+          tc::tmem_ld16(tmem + lanes + T_O + 128 * s + 16 * cb, a);
+          tc::tmem_ld16(tmem + lanes + T_O + 128 * s + 64 + 16 * cb, b);
+          tc::tmem_wait_ld();
+          if (cb == 3) {
+            tc::fence_before_sync();
+            arrive(&B.o_empty[s]);
+          }
+          if (t >= it.t1) continue;
+#pragma unroll
+          for (int x = 0; x < 16; x += 8) {
+            uint32_t y[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              const int u = x + 2 * m;
+              y[m] = pack_bf2(
+                  fmaf(e_prev, __uint_as_float(a[u]), D.scale * __uint_as_float(b[u])),
+                  fmaf(e_prev, __uint_as_float(a[u + 1]), D.scale * __uint_as_float(b[u + 1])));
+              const int2 first =
+                  *reinterpret_cast<const int2*>(&B.colbad[cc & 3][16 * cb + u]);
+              if (first.x <= j) y[m] |= 0x7FFFu;
+              if (first.y <= j) y[m] |= 0x7FFF0000u;
+            }
+            *reinterpret_cast<uint4*>(o + 16 * cb + x) = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        }
+      }
+    }
+  } else if (warp >= 16) {
+    // ------------------------------------------------------- the state
+    const int quad = warp & 3, d = 32 * quad + lane;
+    const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+    const bool mine = 32 * quad < DK;
+    float* row = D.state + (((size_t)it.row * D.HV + h) * DK + d) * D.DV + c0;
+    const float* left = W0 + (size_t)d * D.DV + c0;  // what segment 0 leaves behind
+    // 32 columns at a time; `x` of the functions below is their first column
+    float S[32];
+    auto load = [&](const float* from, float f) {
+#pragma unroll
+      for (int i = 0; i < 32; i += 4) {
+        const float4 y = *reinterpret_cast<const float4*>(from + i);
+        S[i] = fmaf(f, y.x, S[i]), S[i + 1] = fmaf(f, y.y, S[i + 1]);
+        S[i + 2] = fmaf(f, y.z, S[i + 2]), S[i + 3] = fmaf(f, y.w, S[i + 3]);
+      }
+    };
+    auto clear = [&]() {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) S[i] = 0.f;
+    };
+    // what the first `segs` segments leave behind, together
+    auto join = [&](int x, int segs) {
+      clear();
+      double R = 0.0;
+      for (int g = segs - 1; g >= 0; --g) {
+        load(left + (size_t)g * D.HV * plane + x, exp2f((float)R));
+        R += P.Wg[(size_t)(it.slot + g) * D.HV + h];
+      }
+    };
+    auto from_tmem = [&](int x) {
+      uint32_t r[32];
+      tc::tmem_ld32(tmem + lanes + T_S + x, r);
+      tc::tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) S[i] = __uint_as_float(r[i]);
+    };
+    auto store = [&](float* to) {
+#pragma unroll
+      for (int i = 0; i < 32; i += 4)
+        *reinterpret_cast<float4*>(to + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+    };
+    bool ok = true;
+    for (int c = 0; c < n && ok; ++c) {
+      if (STATES) {
+        ok = wait(&B.s_full, c);
+        continue;
+      }
+      if (c > 0) {
+        ok = wait(&B.s_full, c - 1);
+        if (!ok) break;
+        tc::fence_after_sync();
+      }
+      ok = wait(&B.gate_full[c & 1], c >> 1);
+      if (!ok) break;
+      if (mine) {
+        const float tot = B.gate[c & 1].tot;
+#pragma unroll 1
+        for (int x = 0; x < 64; x += 32) {
+          if (c > 0) {
+            from_tmem(x);
+          } else if (it.seg == 0) {
+            clear();
+            load(row + x, 1.f);
+          } else {
+            join(x, it.seg);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(sb + 128 * d + 16 * ((x / 8 + i) ^ (d & 7))) = make_uint4(
+                pack_bf2(S[8 * i], S[8 * i + 1]), pack_bf2(S[8 * i + 2], S[8 * i + 3]),
+                pack_bf2(S[8 * i + 4], S[8 * i + 5]), pack_bf2(S[8 * i + 6], S[8 * i + 7]));
+          uint32_t r[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(S[i] * tot);
+          tc::tmem_st32(tmem + lanes + T_S + x, r);
+        }
+        tc::tmem_wait_st();
+      }
+      tc::fence_before_sync();
+      tc::fence_async_smem();
+      arrive(&B.sb_full);
+      if (lane == 0) mbar_arrive(&B.gate_empty[c & 1]);
+    }
+    if (ok && !STATES) ok = wait(&B.s_full, n - 1);
+    if (ok && STATES) ok = wait(&B.gate_full[(n - 1) & 1], (n - 1) >> 1);
+    if (ok && mine && !B.failed) {
+      tc::fence_after_sync();
+#pragma unroll 1
+      for (int x = 0; x < 64; x += 32) {
+        if (STATES) {
+          from_tmem(x);
+          if (it.seg == 0) load(row + x, exp2f((float)B.g_total));
+          store(const_cast<float*>(left) + (size_t)it.seg * D.HV * plane + x);
+        } else if (it.nseg == 1) {
+          from_tmem(x);
+          store(row + x);
+        } else if (it.seg == 0) {
+          // the only segment that reads the state's row writes it
+          join(x, it.nseg);
+          store(row + x);
+        }
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (B.failed) {
+    // a wait gave up: give copies that may still be in flight time to land
+    const uint64_t tw = globaltimer_ns();
+    while (globaltimer_ns() - tw < kDrainNs) {
+    }
+  }
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+constexpr int chunk_smem(int DK) { return 2 * (512 * DK + 16384) + 32768 + 128 * DK + 8192; }
+
+// Tokens of a segment: so many that the segments of one sequence of T tokens give
+// every SM about four walks, but 512 at least.
+int segment_tokens(int T, int HV, int DV) {
+  const int walks = HV * (DV / 64), want = 4 * num_sms() / walks;
+  if (want <= 1) return (T + CH - 1) / CH * CH;
+  const int L = ((T + want - 1) / want + CH - 1) / CH * CH;
+  return L < 512 ? 512 : L;
+}
+
+// Segments of sequences that have two and more: a sequence of n > L tokens has
+// ceil(n / L) < 2 n / L.
+size_t segment_slots(int T, int L) { return T > L ? 2 * (size_t)T / L : 0; }
+
+size_t prefill_bytes(int T, int HV, int DK, int DV, float** W, double** Wg, void* base) {
+  const size_t slots = segment_slots(T, segment_tokens(T, HV, DV));
+  Carver c(base);
+  float* w = c.take<float>(slots * HV * DK * DV);
+  double* g = c.take<double>(slots * HV + 1);
+  if (W) *W = w, *Wg = g;
+  return c.used();
+}
+
+std::mutex g_attr_mu;
+bool g_attr_done[64] = {false};
+
+int launch_prefill(const DecayParams& D, void* ws, cudaStream_t st) {
+  {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return ER_ECUDA;
+    std::lock_guard<std::mutex> lock(g_attr_mu);
+    if (!g_attr_done[dev]) {
+      const cudaFuncAttribute a = cudaFuncAttributeMaxDynamicSharedMemorySize;
+      if (cudaFuncSetAttribute(k_decay_chunks<64, false>, a, chunk_smem(64)) != cudaSuccess ||
+          cudaFuncSetAttribute(k_decay_chunks<64, true>, a, chunk_smem(64)) != cudaSuccess ||
+          cudaFuncSetAttribute(k_decay_chunks<128, false>, a, chunk_smem(128)) != cudaSuccess ||
+          cudaFuncSetAttribute(k_decay_chunks<128, true>, a, chunk_smem(128)) != cudaSuccess)
+        return ER_ECUDA;
+      g_attr_done[dev] = true;
+    }
+  }
+  ChunkParams P{};
+  P.d = D;
+  P.L = segment_tokens(D.T, D.HV, D.DV);
+  prefill_bytes(D.T, D.HV, D.DK, D.DV, &P.W, &P.Wg, ws);
+  if (!encode_rows(&P.q_map, D.q, false, D.HK * D.DK, D.T, D.ldq * 2, 64, CH) ||
+      !encode_rows(&P.k_map, D.k, false, D.HK * D.DK, D.T, D.ldk * 2, 64, CH) ||
+      !encode_rows(&P.v_map, D.v, false, D.HV * D.DV, D.T, D.ldv * 2, 64, CH))
+    return ER_ECUDA;
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  const size_t segs = (size_t)D.B + (D.T > P.L ? D.T / P.L : 0);
+  const size_t blocks = segs * D.HV * (D.DV / 64);
+  if (blocks > 0x7FFFFFFFu) return ER_EINVAL;
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(DC_THREADS);
+  cfg.dynamicSmemBytes = chunk_smem(D.DK);
+  cfg.stream = st;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  for (int pass = D.T > P.L ? 0 : 1; pass < 2; ++pass) {
+    const auto fn = D.DK == 64 ? (pass ? k_decay_chunks<64, false> : k_decay_chunks<64, true>)
+                               : (pass ? k_decay_chunks<128, false> : k_decay_chunks<128, true>);
+    if (cudaLaunchKernelEx(&cfg, fn, P) != cudaSuccess) return ER_ECUDA;
+    count_launches(1);
+  }
   return launch_status();
 }
 
@@ -102,7 +823,8 @@ int fill(DecayParams& P, float* state, int32_t s_max, const int32_t* seq_ids, co
          int32_t B, int32_t T, const er_decay_shape* sh, const er_bf16* q, int32_t ldq,
          const er_bf16* k, int32_t ldk, const er_bf16* v, int32_t ldv, const float* g, int32_t ldg,
          float scale, er_bf16* o, int32_t ldo, int32_t* dev_error) {
-  if (!shape_ok(sh) || s_max < 1 || B < 0 || B > 65535 || T < 0) return ER_EINVAL;
+  if (!shape_ok(sh) || s_max < 1 || B < 0 || B > 65535 || T < 0 || T > (1 << 30))
+    return ER_EINVAL;
   const int qk = sh->k_heads * sh->k_dim, vo = sh->v_heads * sh->v_dim;
   if (ldq < qk || ldk < qk || ldv < vo || ldo < vo || ldq % 8 || ldk % 8 || ldv % 8 || ldo % 8 ||
       (ldg != 0 && ldg < sh->v_heads))
@@ -131,8 +853,8 @@ using namespace er;
 extern "C" {
 
 size_t er_decay_prefill_workspace_bytes(const er_decay_shape* shape, int32_t B, int32_t T) {
-  if (!shape_ok(shape) || B < 1 || B > 65535 || T < 0) return 0;
-  return 256;
+  if (!shape_ok(shape) || B < 1 || B > 65535 || T < 0 || T > (1 << 30)) return 0;
+  return prefill_bytes(T, shape->v_heads, shape->k_dim, shape->v_dim, nullptr, nullptr, nullptr);
 }
 
 int er_decay_decode(float* state, int32_t s_max, const int32_t* seq_ids, int32_t B,
@@ -145,7 +867,7 @@ int er_decay_decode(float* state, int32_t s_max, const int32_t* seq_ids, int32_t
                       log_decay, ldg, scale, o, ldo, dev_error);
   if (rc != ER_OK || B == 0) return rc;
   if ((rc = error_word(P)) != ER_OK) return rc;
-  return launch_tokens(P, (cudaStream_t)stream);
+  return launch_decode(P, (cudaStream_t)stream);
 }
 
 int er_decay_prefill(float* state, int32_t s_max, const int32_t* seq_ids,
@@ -162,7 +884,7 @@ int er_decay_prefill(float* state, int32_t s_max, const int32_t* seq_ids,
     return ER_EINVAL;
   if (ws_bytes < er_decay_prefill_workspace_bytes(shape, B, T)) return ER_ECAPACITY;
   if ((rc = error_word(P)) != ER_OK) return rc;
-  return launch_tokens(P, (cudaStream_t)stream);
+  return launch_prefill(P, ws, (cudaStream_t)stream);
 }
 
 }  // extern "C"
