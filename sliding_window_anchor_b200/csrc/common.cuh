@@ -52,6 +52,13 @@ __device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
   return (uint32_t)f2bf(lo) | ((uint32_t)f2bf(hi) << 16);
 }
 
+// The same values as pack_bf2 in one packed conversion.
+__device__ __forceinline__ uint32_t pack2_bf(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
 // ------------------------------------------------------ device error word
 
 __device__ __forceinline__ void set_dev_error(int32_t* err, int code) {

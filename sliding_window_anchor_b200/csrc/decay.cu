@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(DD_THREADS) k_decay_decode(const DecayParams P
       o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
     }
     *reinterpret_cast<uint2*>(P.o + b * P.ldo + h * P.DV + c0 + 4 * threadIdx.x) =
-        make_uint2(pack_bf2(P.scale * o.x, P.scale * o.y), pack_bf2(P.scale * o.z, P.scale * o.w));
+        make_uint2(pack2_bf(P.scale * o.x, P.scale * o.y), pack2_bf(P.scale * o.z, P.scale * o.w));
   }
 }
 
@@ -152,8 +152,8 @@ int launch_decode(const DecayParams& P, cudaStream_t st) {
 //   S  <- e^{G_127} S + Σ_j k_j (e^{G_127 - G_j} v_j)ᵀ
 // as four tensor-core products (tcgen05): Q Kᵀ (masked and decayed in registers, back
 // into TMEM as BF16), that times V, Q S (S as BF16), Kᵀ Ṽ.  The state's product is
-// exact to 2^-16: its decayed values Ṽ go in as two BF16 terms, hi + lo; the
-// state itself stays in FP32 in TMEM, where the chunk's decay is applied to it.  Of
+// exact to 2^-24: its decayed values Ṽ go in as three BF16 terms; the state itself
+// stays in FP32 in TMEM, where the chunk's decay is applied to it.  Of
 // o's terms each meets one rounding to BF16 (2^-8), like its result.  G is summed in
 // FP64 and kept as two floats, so that differences are exact however large G is.
 //
@@ -164,12 +164,12 @@ int launch_decode(const DecayParams& P, cudaStream_t st) {
 // segment's chunks are walked from its end, so that all decays are known and no
 // product waits for another.
 //
-// Warps: 0 — TMA; 1 — the products; 2 — decays; 4-11 — Q Kᵀ's rows; 12-15 — Ṽ and o;
-// 16-19 — the state.  Non-finite values of v are kept out of the products of the
+// Warps: 0 — TMA; 1 — the products; 2 — decays; 4-11 — Q Kᵀ's rows; 12-19 — Ṽ and o;
+// 20-23 — the state.  Non-finite values of v are kept out of the products of the
 // tokens in front of them: they enter V as zero, the state as NaN, and o's column is
 // NaN from that token on.
 constexpr int CH = 128;
-constexpr int DC_THREADS = 640;
+constexpr int DC_THREADS = 768;
 constexpr uint64_t kDrainNs = 200000;
 
 struct ChunkParams {
@@ -184,7 +184,11 @@ struct alignas(16) Gates {
   float hi[CH], lo[CH];  // G in log2 units, hi + lo
   float w[CH];           // e^{G_end - G_j}; 0 behind the sequence
   float e[CH];           // scale · e^{G_i}
+  // the decay between rows of a block of 32 and columns of an earlier one, through the
+  // block's first row r: e^{G_i - G_r} and, for blocks 1, 2, 3, e^{G_r - G_j}, j < r
+  float rf[CH], cf[192];
   float tot;
+  int grow;              // a decay above 0: the factors might overflow
 };
 
 struct Item {
@@ -256,24 +260,28 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     k_decay_chunks(const __grid_constant__ ChunkParams P) {
   constexpr int QB = DK * 256;  // bytes of a chunk's q (or k) rows: 64-column blocks of 16 KB
   constexpr int VB = 16384;
-  constexpr int STAGE = 2 * QB + VB;
+  constexpr int STAGE = QB + VB;        // k, v
+  constexpr int NV = STATES ? 2 : 1;    // buffers of Ṽ
   constexpr uint32_t T_P = 0, T_PT = 128, T_S = 192, T_O = 256;  // TMEM columns
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  unsigned char* vt = base + 2 * STAGE;  // Ṽ: hi, lo
-  unsigned char* sb = vt + 2 * VB;       // S in BF16, [DK][64]
+  unsigned char* vt = base + 2 * STAGE;     // Ṽ: three terms
+  unsigned char* qb = vt + 3 * NV * VB;     // q
+  unsigned char* sb = qb + (STATES ? 0 : QB);  // S in BF16, [DK][64]
   struct Shared {
     Gates gate[2];
     int colbad[4][64];  // first token of a chunk with a non-finite v, by column
+    int anybad[4];
     uint64_t full[2], empty[2], gate_full[2], gate_empty[2], o_full[2], o_empty[2];
-    uint64_t p_full, pt_full, pt_empty, vt_full, s_full, sb_full, done;
+    uint64_t vt_empty[2], last;  // STATES
+    uint64_t q_full, q_empty, p_full, pt_full, pt_empty, vt_full, s_full, sb_full, done;
     double g_total;
     Item item;
     uint32_t tmem_base;
     volatile int failed;
   };
-  Shared& B = *reinterpret_cast<Shared*>(sb + DK * 128);
+  Shared& B = *reinterpret_cast<Shared*>(sb + (STATES ? 0 : DK * 128));
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const DecayParams& D = P.d;
   const int slices = D.DV / 64, per = D.HV * slices;
@@ -288,14 +296,18 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       mbar_init(&B.full[i], 1);
       mbar_init(&B.empty[i], 1);
       mbar_init(&B.gate_full[i], 1);
-      mbar_init(&B.gate_empty[i], STATES ? 4 : 16);
+      mbar_init(&B.gate_empty[i], STATES ? 8 : 20);
       mbar_init(&B.o_full[i], 1);
-      mbar_init(&B.o_empty[i], 4);
+      mbar_init(&B.vt_empty[i], 1);
+      mbar_init(&B.o_empty[i], 8);
     }
+    mbar_init(&B.last, 1);
+    mbar_init(&B.q_full, 1);
+    mbar_init(&B.q_empty, 1);
     mbar_init(&B.p_full, 1);
     mbar_init(&B.pt_full, 8);
     mbar_init(&B.pt_empty, 1);
-    mbar_init(&B.vt_full, 4);
+    mbar_init(&B.vt_full, 8);
     mbar_init(&B.s_full, 1);
     mbar_init(&B.sb_full, 4);
     mbar_init(&B.done, 1);
@@ -341,14 +353,18 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         ok = mbar_wait(&B.empty[s], ((c >> 1) & 1) ^ 1, D.err);
         if (!ok) break;
         unsigned char* st = base + s * STAGE;
-        mbar_arrive_expect_tx(&B.full[s], STATES ? QB + VB : STAGE);
+        mbar_arrive_expect_tx(&B.full[s], STAGE);
 #pragma unroll
-        for (int x = 0; x < DK / 64; ++x) {
-          tc::tma_load_2d(st + QB + 16384 * x, &P.k_map, DK * hk + 64 * x, t, &B.full[s]);
-          if (!STATES)
-            tc::tma_load_2d(st + 16384 * x, &P.q_map, DK * hk + 64 * x, t, &B.full[s]);
-        }
-        tc::tma_load_2d(st + 2 * QB, &P.v_map, D.DV * h + c0, t, &B.full[s]);
+        for (int x = 0; x < DK / 64; ++x)
+          tc::tma_load_2d(st + 16384 * x, &P.k_map, DK * hk + 64 * x, t, &B.full[s]);
+        tc::tma_load_2d(st + QB, &P.v_map, D.DV * h + c0, t, &B.full[s]);
+        if (STATES) continue;
+        ok = mbar_wait(&B.q_empty, (c & 1) ^ 1, D.err);
+        if (!ok) break;
+        mbar_arrive_expect_tx(&B.q_full, QB);
+#pragma unroll
+        for (int x = 0; x < DK / 64; ++x)
+          tc::tma_load_2d(qb + 16384 * x, &P.q_map, DK * hk + 64 * x, t, &B.q_full);
       }
       if (!ok) B.failed = 1;
     }
@@ -360,9 +376,14 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       constexpr uint32_t id_o = tc::idesc_bf16(128, 64, false, true);
       constexpr uint32_t id_s = tc::idesc_bf16(128, 64, true, true);
       const uint32_t b0 = smem_u32(base), v0 = smem_u32(vt), s0 = smem_u32(sb);
+      const uint32_t q = smem_u32(qb);
       bool ok = true;
-      auto scores = [&](int s) {  // Q Kᵀ
-        const uint32_t q = b0 + s * STAGE, k = q + QB;
+      auto scores = [&](int c) {  // Q Kᵀ
+        ok = mbar_wait(&B.q_full, c & 1, D.err) &&
+             mbar_wait(&B.full[c & 1], (c >> 1) & 1, D.err);
+        if (!ok) return;
+        tc::fence_after_sync();
+        const uint32_t k = b0 + (c & 1) * STAGE;
 #pragma unroll
         for (int kk = 0; kk < DK / 16; ++kk) {
           const uint32_t at = 16384 * (kk >> 2) + 32 * (kk & 3);
@@ -371,16 +392,11 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         }
         tc::commit(&B.p_full);
       };
+      if (!STATES) scores(0);
       for (int c = 0; c < n && ok; ++c) {
         const int s = c & 1, ph = (c >> 1) & 1;
-        const uint32_t q = b0 + s * STAGE, k = q + QB, v = k + QB;
+        const uint32_t k = b0 + s * STAGE, v = k + QB;
         if (!STATES) {
-          if (c == 0) {
-            ok = mbar_wait(&B.full[0], 0, D.err);
-            if (!ok) break;
-            tc::fence_after_sync();
-            scores(0);
-          }
           // Q S
           ok = mbar_wait(&B.sb_full, c & 1, D.err) && mbar_wait(&B.o_empty[s], ph ^ 1, D.err);
           if (!ok) break;
@@ -390,6 +406,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
             tc::mma_bf16(tmem + T_O + 128 * s,
                          tc::desc_sw128(q + 16384 * (kk >> 2) + 32 * (kk & 3), 16, 1024),
                          tc::desc_sw128(s0 + 2048 * kk, 8192, 1024), id_o, kk > 0);
+          tc::commit(&B.q_empty);
         } else {
           ok = mbar_wait(&B.full[s], ph, D.err);
           if (!ok) break;
@@ -399,17 +416,18 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         if (!ok) break;
         tc::fence_after_sync();
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
+        for (int part = 0; part < 3; ++part)
 #pragma unroll
           for (int kk = 0; kk < CH / 16; ++kk)
             tc::mma_bf16(tmem + T_S, tc::desc_sw128(k + 2048 * kk, 16384, 1024),
-                         tc::desc_sw128(v0 + VB * part + 2048 * kk, 8192, 1024), id_s,
-                         !STATES || c > 0 || part > 0 || kk > 0);
-        tc::commit(&B.s_full);
+                         tc::desc_sw128(v0 + VB * (3 * (c & (NV - 1)) + part) + 2048 * kk, 8192, 1024),
+                         id_s, !STATES || c > 0 || part > 0 || kk > 0);
         if (STATES) {
+          tc::commit(&B.vt_empty[s]);
           tc::commit(&B.empty[s]);
           continue;
         }
+        tc::commit(&B.s_full);
         // the masked products times V
         ok = mbar_wait(&B.pt_full, c & 1, D.err);
         if (!ok) break;
@@ -421,14 +439,10 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         tc::commit(&B.o_full[s]);
         tc::commit(&B.pt_empty);
         tc::commit(&B.empty[s]);
-        if (c + 1 < n) {
-          ok = mbar_wait(&B.full[s ^ 1], ((c + 1) >> 1) & 1, D.err);
-          if (!ok) break;
-          tc::fence_after_sync();
-          scores(s ^ 1);
-        }
+        if (c + 1 < n) scores(c + 1);
       }
       if (!ok) B.failed = 1;
+      if (STATES) tc::commit(&B.last);
       tc::commit(&B.done);
       mbar_wait(&B.done, 0, D.err);  // nothing is on the tensor cores at exit
     }
@@ -440,9 +454,11 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     for (int c = 0; c < n; ++c) {
       const int t = it.t0 + CH * (STATES ? n - 1 - c : c) + 4 * lane;
       double G[4];
+      bool up = false;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float g = t + i < it.t1 ? D.g[(t + i) * D.ldg + h] : 0.f;
+        up |= g > 0.f;
         if (g < -1000.f) g = -1000.f;  // e^-1000 is 0, and -inf has no differences
         G[i] = (double)g * kLog2e + (i ? G[i - 1] : 0.0);
       }
@@ -453,6 +469,11 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         if (lane >= m) sum += x;
       }
       const double front = sum - G[3], total = __shfl_sync(0xffffffffu, sum, 31);
+      const double first = front + G[0], own = __shfl_sync(0xffffffffu, first, lane & ~7);
+      double later[3];  // G at the first rows of blocks 1, 2, 3
+#pragma unroll
+      for (int q = 1; q < 4; ++q) later[q - 1] = __shfl_sync(0xffffffffu, first, 8 * q);
+      up = __any_sync(0xffffffffu, up);
       if (!wait(&B.gate_empty[c & 1], ((c >> 1) & 1) ^ 1)) break;
       Gates& g = B.gate[c & 1];
 #pragma unroll
@@ -462,9 +483,14 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         g.hi[4 * lane + i] = hi;
         g.lo[4 * lane + i] = (float)(x - (double)hi);
         g.w[4 * lane + i] = t + i < it.t1 ? exp2f((float)(R + (total - x))) : 0.f;
+        if (STATES) continue;
         g.e[4 * lane + i] = D.scale * exp2f(hi);
+        g.rf[4 * lane + i] = ex2((float)(x - own));
+#pragma unroll
+        for (int q = 1; q < 4; ++q)
+          if (lane < 8 * q) g.cf[16 * q * (q - 1) + 4 * lane + i] = ex2((float)(later[q - 1] - x));
       }
-      if (lane == 0) g.tot = exp2f((float)total);
+      if (lane == 0) g.tot = exp2f((float)total), g.grow = up;
       if (STATES) {
         R += total;
         if (lane == 0) B.g_total = R;
@@ -487,25 +513,42 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
           break;
         tc::fence_after_sync();
         const Gates& g = B.gate[c & 1];
-        const float hi = g.hi[i], lo = g.lo[i];
+        const bool factors = !g.grow;
 #pragma unroll 1
         for (int cb = half; cb <= quad; cb += 2) {
-          uint32_t r[32], o[16];
+          uint32_t r[32];
           tc::tmem_ld32(tmem + lanes + T_P + 32 * cb, r);
           tc::tmem_wait_ld();
-          // a column right of the diagonal is masked, whatever it holds
-          const int last = cb == quad ? lane : 31;
+          if (cb < quad && factors) {
+            const float rf = g.rf[i];
+            const float* cf = &g.cf[16 * quad * (quad - 1) + 32 * cb];
 #pragma unroll
-          for (int x = 0; x < 32; x += 4) {
-            const float4 gh = *reinterpret_cast<const float4*>(&g.hi[32 * cb + x]);
-            const float4 gl = *reinterpret_cast<const float4*>(&g.lo[32 * cb + x]);
-            const float p0 = __uint_as_float(r[x]) * ex2((hi - gh.x) + (lo - gl.x));
-            const float p1 = __uint_as_float(r[x + 1]) * ex2((hi - gh.y) + (lo - gl.y));
-            const float p2 = __uint_as_float(r[x + 2]) * ex2((hi - gh.z) + (lo - gl.z));
-            const float p3 = __uint_as_float(r[x + 3]) * ex2((hi - gh.w) + (lo - gl.w));
-            o[x / 2] = pack_bf2(x <= last ? p0 : 0.f, x + 1 <= last ? p1 : 0.f);
-            o[x / 2 + 1] = pack_bf2(x + 2 <= last ? p2 : 0.f, x + 3 <= last ? p3 : 0.f);
+            for (int x = 0; x < 32; x += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(cf + x);
+              r[x / 2] = pack2_bf(__uint_as_float(r[x]) * (rf * f.x),
+                                  __uint_as_float(r[x + 1]) * (rf * f.y));
+              r[x / 2 + 1] = pack2_bf(__uint_as_float(r[x + 2]) * (rf * f.z),
+                                      __uint_as_float(r[x + 3]) * (rf * f.w));
+            }
+          } else {
+            // a column right of the diagonal is masked, whatever it holds
+            const float hi = g.hi[i], lo = g.lo[i];
+            const int last = cb == quad ? lane : 31;
+#pragma unroll
+            for (int x = 0; x < 32; x += 4) {
+              const float4 gh = *reinterpret_cast<const float4*>(&g.hi[32 * cb + x]);
+              const float4 gl = *reinterpret_cast<const float4*>(&g.lo[32 * cb + x]);
+              const float p0 = __uint_as_float(r[x]) * ex2((hi - gh.x) + (lo - gl.x));
+              const float p1 = __uint_as_float(r[x + 1]) * ex2((hi - gh.y) + (lo - gl.y));
+              const float p2 = __uint_as_float(r[x + 2]) * ex2((hi - gh.z) + (lo - gl.z));
+              const float p3 = __uint_as_float(r[x + 3]) * ex2((hi - gh.w) + (lo - gl.w));
+              r[x / 2] = pack2_bf(x <= last ? p0 : 0.f, x + 1 <= last ? p1 : 0.f);
+              r[x / 2 + 1] = pack2_bf(x + 2 <= last ? p2 : 0.f, x + 3 <= last ? p3 : 0.f);
+            }
           }
+          uint32_t o[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) o[x] = r[x];
           tc::tmem_st16(tmem + lanes + T_PT + 16 * cb, o);
         }
         tc::tmem_wait_st();
@@ -514,40 +557,48 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         if (lane == 0) mbar_arrive(&B.gate_empty[c & 1]);
       }
     }
-  } else if (warp >= 12 && warp < 16) {
-    // ------------------------------------------------------- Ṽ, then o
-    const int quad = warp & 3, j = 32 * quad + lane;
+  } else if (warp >= 12 && warp < 20) {
+    // ------------------------------- Ṽ, then o: 32 columns of a row a thread
+    const int quad = warp & 3, half = (warp - 12) >> 2, j = 32 * quad + lane;
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+    const int tid = threadIdx.x - 32 * 12;
     float e = 0.f;
     for (int c = 0; c <= n; ++c) {
       const float e_prev = e;
       if (c < n) {
         const int s = c & 1, t = it.t0 + CH * (STATES ? n - 1 - c : c) + j;
-        if (!STATES && threadIdx.x - 384 < 64) B.colbad[c & 3][threadIdx.x - 384] = CH;
-        named_bar_sync(1, 128);
+        if (!STATES) {
+          if (tid < 64) B.colbad[c & 3][tid] = CH;
+          if (tid == 64) B.anybad[c & 3] = 0;
+          named_bar_sync(1, 256);
+        }
         if (!wait(&B.full[s], c >> 1) || !wait(&B.gate_full[s], c >> 1) ||
-            (c > 0 && !wait(&B.s_full, c - 1)))
+            !(STATES ? wait(&B.vt_empty[s], (c >> 1) + 1) : c == 0 || wait(&B.s_full, c - 1)))
           break;
         const float w = B.gate[s].w[j];
-        e = B.gate[s].e[j];
+        if (!STATES) e = B.gate[s].e[j];
         unsigned char* st = base + s * STAGE;
-        unsigned char* v = st + 2 * QB + 128 * j;
+        unsigned char* v = st + QB + 128 * j;
+        unsigned char* to = vt + 3 * VB * (c & (NV - 1)) + 128 * j;
         const int sw = j & 7;
         if (t < it.t1) {
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            uint4* at = reinterpret_cast<uint4*>(v + 16 * (x ^ sw));
-            const uint4 y = *at;
-            uint32_t in[4] = {y.x, y.y, y.z, y.w}, hi[4], lo[4];
-            bool bad = false;
+          for (int y = 0; y < 4; ++y) {
+            const int x = 4 * half + y, at = 16 * (x ^ sw);
+            const uint4 word = *reinterpret_cast<const uint4*>(v + at);
+            uint32_t in[4] = {word.x, word.y, word.z, word.w}, hi[4], mid[4], lo[4];
+            float odd = 0.f;  // NaN once a value of v is infinite or NaN
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-              const float a = bf_lo(in[m]) * w, b = bf_hi(in[m]) * w;
-              hi[m] = pack_bf2(a, b);
-              lo[m] = pack_bf2(a - bf_lo(hi[m]), b - bf_hi(hi[m]));
-              bad |= (in[m] & 0x7F80u) == 0x7F80u || (in[m] & 0x7F800000u) == 0x7F800000u;
+              float a = bf_lo(in[m]), b = bf_hi(in[m]);
+              odd = fmaf(a, 0.f, fmaf(b, 0.f, odd));
+              a *= w, b *= w;
+              hi[m] = pack2_bf(a, b);
+              a -= bf_lo(hi[m]), b -= bf_hi(hi[m]);
+              mid[m] = pack2_bf(a, b);
+              lo[m] = pack2_bf(a - bf_lo(mid[m]), b - bf_hi(mid[m]));
             }
-            if (bad) {
+            if (odd != 0.f) {
 #pragma unroll
               for (int m = 0; m < 4; ++m) {
                 if ((in[m] & 0x7F80u) == 0x7F80u) {
@@ -561,24 +612,26 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
                   hi[m] |= 0x7FFF0000u;
                 }
               }
-              *at = make_uint4(in[0], in[1], in[2], in[3]);
+              B.anybad[c & 3] = 1;
+              *reinterpret_cast<uint4*>(v + at) = make_uint4(in[0], in[1], in[2], in[3]);
             }
-            *reinterpret_cast<uint4*>(vt + 128 * j + 16 * (x ^ sw)) =
-                make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(vt + VB + 128 * j + 16 * (x ^ sw)) =
-                make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            *reinterpret_cast<uint4*>(to + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(to + VB + at) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+            *reinterpret_cast<uint4*>(to + 2 * VB + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
         } else {
           // behind the sequence: another one's rows, or nothing
           const uint4 z = make_uint4(0, 0, 0, 0);
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            *reinterpret_cast<uint4*>(v + 16 * x) = z;
-            *reinterpret_cast<uint4*>(vt + 128 * j + 16 * x) = z;
-            *reinterpret_cast<uint4*>(vt + VB + 128 * j + 16 * x) = z;
+          for (int y = 0; y < 4; ++y) {
+            const int at = 16 * (4 * half + y);
+            *reinterpret_cast<uint4*>(v + at) = z;
 #pragma unroll
-            for (int y = 0; y < DK / 64; ++y)
-              *reinterpret_cast<uint4*>(st + QB + 16384 * y + 128 * j + 16 * x) = z;
+            for (int part = 0; part < 3; ++part)
+              *reinterpret_cast<uint4*>(to + part * VB + at) = z;
+#pragma unroll
+            for (int x = 0; x < DK / 64; ++x)
+              *reinterpret_cast<uint4*>(st + 16384 * x + 128 * j + at) = z;
           }
         }
         tc::fence_async_smem();
@@ -587,41 +640,44 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       }
       if (!STATES && c > 0) {
         const int cc = c - 1, s = cc & 1, t = it.t0 + CH * cc + j;
-        if (c == n) named_bar_sync(1, 128);  // the last chunk's marks
+        if (c == n) named_bar_sync(1, 256);  // the last chunk's marks
         if (!wait(&B.o_full[s], cc >> 1)) break;
         tc::fence_after_sync();
-        uint16_t* o = D.o + t * D.ldo + h * D.DV + c0;
+        const int col = 32 * half;
+        uint16_t* o = D.o + t * D.ldo + h * D.DV + c0 + col;
+        const bool marks = B.anybad[cc & 3] != 0;
 #pragma unroll
-        for (int cb = 0; cb < 4; ++cb) {
+        for (int cb = 0; cb < 2; ++cb) {
           uint32_t a[16], b[16];
-          tc::tmem_ld16(tmem + lanes + T_O + 128 * s + 16 * cb, a);
-          tc::tmem_ld16(tmem + lanes + T_O + 128 * s + 64 + 16 * cb, b);
+          tc::tmem_ld16(tmem + lanes + T_O + 128 * s + col + 16 * cb, a);
+          tc::tmem_ld16(tmem + lanes + T_O + 128 * s + 64 + col + 16 * cb, b);
           tc::tmem_wait_ld();
-          if (cb == 3) {
+          if (cb == 1) {
             tc::fence_before_sync();
             arrive(&B.o_empty[s]);
           }
           if (t >= it.t1) continue;
+          uint32_t y[8];
 #pragma unroll
-          for (int x = 0; x < 16; x += 8) {
-            uint32_t y[4];
+          for (int m = 0; m < 8; ++m)
+            y[m] = pack2_bf(
+                fmaf(e_prev, __uint_as_float(a[2 * m]), D.scale * __uint_as_float(b[2 * m])),
+                fmaf(e_prev, __uint_as_float(a[2 * m + 1]),
+                     D.scale * __uint_as_float(b[2 * m + 1])));
+          if (marks) {
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              const int u = x + 2 * m;
-              y[m] = pack_bf2(
-                  fmaf(e_prev, __uint_as_float(a[u]), D.scale * __uint_as_float(b[u])),
-                  fmaf(e_prev, __uint_as_float(a[u + 1]), D.scale * __uint_as_float(b[u + 1])));
-              const int2 first =
-                  *reinterpret_cast<const int2*>(&B.colbad[cc & 3][16 * cb + u]);
-              if (first.x <= j) y[m] |= 0x7FFFu;
-              if (first.y <= j) y[m] |= 0x7FFF0000u;
+            for (int m = 0; m < 8; ++m) {
+              const int u = col + 16 * cb + 2 * m;
+              if (B.colbad[cc & 3][u] <= j) y[m] |= 0x7FFFu;
+              if (B.colbad[cc & 3][u + 1] <= j) y[m] |= 0x7FFF0000u;
             }
-            *reinterpret_cast<uint4*>(o + 16 * cb + x) = make_uint4(y[0], y[1], y[2], y[3]);
           }
+          *reinterpret_cast<uint4*>(o + 16 * cb) = make_uint4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<uint4*>(o + 16 * cb + 8) = make_uint4(y[4], y[5], y[6], y[7]);
         }
       }
     }
-  } else if (warp >= 16) {
+  } else if (warp >= 20) {
     // ------------------------------------------------------- the state
     const int quad = warp & 3, d = 32 * quad + lane;
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
@@ -664,11 +720,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         *reinterpret_cast<float4*>(to + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
     };
     bool ok = true;
-    for (int c = 0; c < n && ok; ++c) {
-      if (STATES) {
-        ok = wait(&B.s_full, c);
-        continue;
-      }
+    for (int c = 0; !STATES && c < n; ++c) {
       if (c > 0) {
         ok = wait(&B.s_full, c - 1);
         if (!ok) break;
@@ -691,8 +743,8 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             *reinterpret_cast<uint4*>(sb + 128 * d + 16 * ((x / 8 + i) ^ (d & 7))) = make_uint4(
-                pack_bf2(S[8 * i], S[8 * i + 1]), pack_bf2(S[8 * i + 2], S[8 * i + 3]),
-                pack_bf2(S[8 * i + 4], S[8 * i + 5]), pack_bf2(S[8 * i + 6], S[8 * i + 7]));
+                pack2_bf(S[8 * i], S[8 * i + 1]), pack2_bf(S[8 * i + 2], S[8 * i + 3]),
+                pack2_bf(S[8 * i + 4], S[8 * i + 5]), pack2_bf(S[8 * i + 6], S[8 * i + 7]));
           uint32_t r[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(S[i] * tot);
@@ -705,8 +757,8 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       arrive(&B.sb_full);
       if (lane == 0) mbar_arrive(&B.gate_empty[c & 1]);
     }
-    if (ok && !STATES) ok = wait(&B.s_full, n - 1);
-    if (ok && STATES) ok = wait(&B.gate_full[(n - 1) & 1], (n - 1) >> 1);
+    // STATES: g_total was written in front of the last gate_full, behind which is `last`
+    if (ok) ok = STATES ? wait(&B.last, 0) : wait(&B.s_full, n - 1);
     if (ok && mine && !B.failed) {
       tc::fence_after_sync();
 #pragma unroll 1
@@ -740,7 +792,12 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   }
 }
 
-constexpr int chunk_smem(int DK) { return 2 * (512 * DK + 16384) + 32768 + 128 * DK + 8192; }
+// k, v twice; three terms of Ṽ, q and S (twice the terms for STATES); the rest, alignment.
+constexpr int chunk_smem(int DK) {
+  constexpr int terms = 3 * 16384;
+  const int main = terms + 256 * DK + 128 * DK;
+  return 2 * (256 * DK + 16384) + (main > 2 * terms ? main : 2 * terms) + 10240;
+}
 
 // Tokens of a segment: so many that the segments of one sequence of T tokens give
 // every SM about four walks, but 512 at least.

@@ -92,8 +92,8 @@ __device__ __forceinline__ void finish_four(const FusedParams& P, int t, int f,
       uint2 a = make_uint2(0u, 0u);
       if (P.residual) a = *reinterpret_cast<const uint2*>(r);
       *reinterpret_cast<uint2*>(y) =
-          make_uint2(pack_bf2(v[0] + bf_lo(a.x), v[1] + bf_hi(a.x)),
-                     pack_bf2(v[2] + bf_lo(a.y), v[3] + bf_hi(a.y)));
+          make_uint2(pack2_bf(v[0] + bf_lo(a.x), v[1] + bf_hi(a.x)),
+                     pack2_bf(v[2] + bf_lo(a.y), v[3] + bf_hi(a.y)));
       return;
     }
 #pragma unroll
@@ -543,10 +543,10 @@ __global__ void __launch_bounds__(DN_THREADS, 1) k_dense(const __grid_constant__
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint4 o;
-              o.x = pack_bf2(v[8 * i], v[8 * i + 1]);
-              o.y = pack_bf2(v[8 * i + 2], v[8 * i + 3]);
-              o.z = pack_bf2(v[8 * i + 4], v[8 * i + 5]);
-              o.w = pack_bf2(v[8 * i + 6], v[8 * i + 7]);
+              o.x = pack2_bf(v[8 * i], v[8 * i + 1]);
+              o.y = pack2_bf(v[8 * i + 2], v[8 * i + 3]);
+              o.z = pack2_bf(v[8 * i + 4], v[8 * i + 5]);
+              o.w = pack2_bf(v[8 * i + 6], v[8 * i + 7]);
               *reinterpret_cast<uint4*>(stg + 128 * lane +
                                         16 * ((4 * (cb & 1) + i) ^ (lane & 7))) = o;
             }
