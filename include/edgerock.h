@@ -328,7 +328,7 @@ int er_gated_linear(const er_bf16* x, int32_t ldx, int32_t T, const er_bf16* w_g
  *          Value head h reads q and k of head h / (v_heads / k_heads).
  *   log_decay FP32 rows of [v_heads] natural logs, ldg apart, or ldg = 0: one
  *          row for every token.  Any value but +inf: 0 keeps the state, -inf
- *          forgets it (values below -1000 count as -inf), NaN spreads as in the
+ *          forgets it (so does every value below -150), NaN spreads as in the
  *          formula.
  *   o      BF16 rows of [v_heads][v_dim], ldo apart, rounded once.
  * er_decay_decode: one token for each of B sequences, row b the token of

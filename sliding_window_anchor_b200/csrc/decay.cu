@@ -155,7 +155,8 @@ int launch_decode(const DecayParams& P, cudaStream_t st) {
 // exact to 2^-24: its decayed values Ṽ go in as three BF16 terms; the state itself
 // stays in FP32 in TMEM, where the chunk's decay is applied to it.  Of
 // o's terms each meets one rounding to BF16 (2^-8), like its result.  G is summed in
-// FP64 and kept as two floats, so that differences are exact however large G is.
+// FP64; differences go to FP32 relative to a row of the same 32 (with log-decays of -150
+// at least, they are off by 2^-12 at most).
 //
 // A CTA walks 64 columns of one value head through one segment of a sequence.
 // Long sequences are cut into segments of L tokens that are walked at the same time:
@@ -164,16 +165,20 @@ int launch_decode(const DecayParams& P, cudaStream_t st) {
 // segment's chunks are walked from its end, so that all decays are known and no
 // product waits for another.
 //
-// Warps: 0 — TMA; 1 — the products; 2 — decays; 4-11 — Q Kᵀ's rows; 12-19 — Ṽ and o;
-// 20-23 — the state.  Non-finite values of v are kept out of the products of the
+// Warps, by the TMEM lanes (32 · (warp % 4)..) that they can reach and by warp / 4: below
+// warp / 4 = 4 one for each block of 32 x 32 of Q Kᵀ on and below the diagonal (lanes
+// of block row r: r + 1 of them), the rest of these for TMA, the products and the
+// decays; 4 and 5 — Ṽ and o; 6 — the state.  Non-finite values of v are kept out of the products of the
 // tokens in front of them: they enter V as zero, the state as NaN, and o's column is
 // NaN from that token on.
 constexpr int CH = 128;
-constexpr int DC_THREADS = 768;
+constexpr int DC_THREADS = 896;
+constexpr int DC_TMA = 4, DC_MMA = 8, DC_GATES = 12;  // warps that have no block
 constexpr uint64_t kDrainNs = 200000;
 
 struct ChunkParams {
   CUtensorMap q_map, k_map, v_map;  // rows of [T][heads · dim], boxes 64 x 128
+  CUtensorMap o_map;                // the same, boxes 32 x 32
   DecayParams d;
   int L;        // tokens of a segment (a multiple of CH)
   float* W;     // [slots][HV][DK][DV] what a segment leaves, for sequences of two and more
@@ -181,15 +186,15 @@ struct ChunkParams {
 };
 
 struct alignas(16) Gates {
-  float hi[CH], lo[CH];  // G in log2 units, hi + lo
-  float w[CH];           // e^{G_end - G_j}; 0 behind the sequence
-  float e[CH];           // scale · e^{G_i}
-  // the decay between rows of a block of 32 and columns of an earlier one, through the
-  // block's first row r: e^{G_i - G_r} and, for blocks 1, 2, 3, e^{G_r - G_j}, j < r
-  float rf[CH], cf[192];
+  float w[CH];  // e^{G_127 - G_j}; 0 behind the sequence
+  float e[CH];  // |scale| · e^{G_i}
+  // |scale| · e^{G_i - G_j} is 2^(row[i] + col[..][j]), through the first row r of i's
+  // block of 32: log2 of |scale| · e^{G_i - G_r}, and for every block row log2 of
+  // e^{G_r - G_j} for the columns up to its end
+  float row[CH], col[32 * (1 + 2 + 3 + 4)];
   float tot;
-  int grow;              // a decay above 0: the factors might overflow
 };
+__device__ __forceinline__ constexpr int col_at(int block) { return 16 * block * (block + 1); }
 
 struct Item {
   int found, row, b, seg, nseg, slot, t0, t1;
@@ -201,6 +206,7 @@ __device__ __forceinline__ void find_item(const DecayParams& P, int L, int index
   int acc = 0, slots = 0;
   long long tokens = 0;
   Item it{};
+#pragma unroll 1
   for (int b0 = 0; b0 < P.B; b0 += 32) {
     const int b = b0 + lane;
     int n = 0, begin = 0, end = 0, row = 0;
@@ -255,6 +261,57 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// x · 0 + y on two BF16 values.
+__device__ __forceinline__ uint32_t times_zero(uint32_t x, uint32_t y) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(x), "r"(0u), "r"(y));
+  return d;
+}
+
+// The roles' loops run at the same time and share the SM's instruction cache: with
+// everything unrolled and inlined (78 KB) they waited for instructions, so what runs
+// rarely is a function, and loops stay loops where that costs little.
+// The rest of a wait, bounded as mbar_wait: the hardware may hold the thread for the
+// hinted time, so that a waiting warp issues little.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, int32_t* err) {
+  constexpr uint32_t kHintNs = 20000;
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(kHintNs)
+        : "memory");
+    if (ok) return true;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      set_dev_error(err, ER_ETIMEOUT);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, int phase, int32_t* err) {
+  return mbar_try_wait(bar, (uint32_t)phase & 1u) || wait_slow(bar, (uint32_t)phase & 1u, err);
+}
+
+// A row's infinite and NaN values among 32 columns of v: zero in v, NaN in the
+// first term of Ṽ, and noted by column.
+__device__ __noinline__ void mark_row(unsigned char* v, unsigned char* terms, int sw, int half,
+                                      int j, int* colbad, int* anybad) {
+#pragma unroll 1
+  for (int x = 4 * half; x < 4 * half + 4; ++x)
+#pragma unroll 1
+    for (int m = 0; m < 8; ++m) {
+      uint16_t* at = reinterpret_cast<uint16_t*>(v + 16 * (x ^ sw)) + m;
+      if ((*at & 0x7F80u) != 0x7F80u) continue;
+      *at = 0;
+      reinterpret_cast<uint16_t*>(terms + 16 * (x ^ sw))[m] = 0x7FFF;
+      atomicMin(&colbad[8 * x + m], j);
+      *anybad = 1;
+    }
+}
+
 template <int DK, bool STATES>
 __global__ void __launch_bounds__(DC_THREADS, 1)
     k_decay_chunks(const __grid_constant__ ChunkParams P) {
@@ -262,26 +319,29 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   constexpr int VB = 16384;
   constexpr int STAGE = QB + VB;        // k, v
   constexpr int NV = STATES ? 2 : 1;    // buffers of Ṽ
-  constexpr uint32_t T_P = 0, T_PT = 128, T_S = 192, T_O = 256;  // TMEM columns
+  // TMEM columns: Q Kᵀ, and that masked, as BF16, in the first 16 columns of each 32; the
+  // state's sums, one for each term of Ṽ; the masked products times V; Q S, twice
+  constexpr uint32_t T_P = 0, T_S = 128, T_O = 320, T_OS = 384;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   unsigned char* vt = base + 2 * STAGE;     // Ṽ: three terms
   unsigned char* qb = vt + 3 * NV * VB;     // q
   unsigned char* sb = qb + (STATES ? 0 : QB);  // S in BF16, [DK][64]
+  unsigned char* ob = sb + (STATES ? 0 : DK * 128);  // o on its way out
   struct Shared {
     Gates gate[2];
     int colbad[4][64];  // first token of a chunk with a non-finite v, by column
     int anybad[4];
-    uint64_t full[2], empty[2], gate_full[2], gate_empty[2], o_full[2], o_empty[2];
+    uint64_t full[2], empty[2], gate_full[2], gate_empty[2];
     uint64_t vt_empty[2], last;  // STATES
-    uint64_t q_full, q_empty, p_full, pt_full, pt_empty, vt_full, s_full, sb_full, done;
+    uint64_t o_full, o_empty[2], q_full, q_empty, p_full, pt_full, vt_full, s_full, sb_full, done;
     double g_total;
     Item item;
     uint32_t tmem_base;
     volatile int failed;
   };
-  Shared& B = *reinterpret_cast<Shared*>(sb + (STATES ? 0 : DK * 128));
+  Shared& B = *reinterpret_cast<Shared*>(ob + (STATES ? 0 : 16384));
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const DecayParams& D = P.d;
   const int slices = D.DV / 64, per = D.HV * slices;
@@ -296,17 +356,17 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       mbar_init(&B.full[i], 1);
       mbar_init(&B.empty[i], 1);
       mbar_init(&B.gate_full[i], 1);
-      mbar_init(&B.gate_empty[i], STATES ? 8 : 20);
-      mbar_init(&B.o_full[i], 1);
+      mbar_init(&B.gate_empty[i], STATES ? 8 : 22);
       mbar_init(&B.vt_empty[i], 1);
-      mbar_init(&B.o_empty[i], 8);
     }
     mbar_init(&B.last, 1);
+    mbar_init(&B.o_full, 1);
+    mbar_init(&B.o_empty[0], 8);
+    mbar_init(&B.o_empty[1], 8);
     mbar_init(&B.q_full, 1);
     mbar_init(&B.q_empty, 1);
     mbar_init(&B.p_full, 1);
-    mbar_init(&B.pt_full, 8);
-    mbar_init(&B.pt_empty, 1);
+    mbar_init(&B.pt_full, 10);
     mbar_init(&B.vt_full, 8);
     mbar_init(&B.s_full, 1);
     mbar_init(&B.sb_full, 4);
@@ -323,7 +383,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     if (threadIdx.x == 0) set_dev_error(D.err, ER_EINVAL);
     return;
   }
-  if (warp == 1) tc::tmem_alloc(&B.tmem_base, 512);
+  if (warp == DC_MMA) tc::tmem_alloc(&B.tmem_base, 512);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -334,8 +394,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
 
   // a wait of a whole warp: false (in every lane) when it gave up or another one did
   auto wait = [&](uint64_t* bar, int phase) {
-    const bool ok = mbar_wait(bar, (uint32_t)phase & 1u, D.err);
-    if (__all_sync(0xffffffffu, ok)) return true;
+    if (__all_sync(0xffffffffu, wait_bar(bar, phase, D.err))) return true;
     B.failed = 1;
     return false;
   };
@@ -344,13 +403,14 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     if (lane == 0) mbar_arrive(bar);
   };
 
-  if (warp == 0) {
+  if (warp == DC_TMA) {
     // ------------------------------------------------------------- TMA
     if (tc::elect_one()) {
       bool ok = true;
-      for (int c = 0; c < n && ok; ++c) {
+#pragma unroll 1
+      for (int c = 0; c < n; ++c) {
         const int s = c & 1, t = it.t0 + CH * (STATES ? n - 1 - c : c);
-        ok = mbar_wait(&B.empty[s], ((c >> 1) & 1) ^ 1, D.err);
+        ok = wait_bar(&B.empty[s], (c >> 1) + 1, D.err);
         if (!ok) break;
         unsigned char* st = base + s * STAGE;
         mbar_arrive_expect_tx(&B.full[s], STAGE);
@@ -359,7 +419,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
           tc::tma_load_2d(st + 16384 * x, &P.k_map, DK * hk + 64 * x, t, &B.full[s]);
         tc::tma_load_2d(st + QB, &P.v_map, D.DV * h + c0, t, &B.full[s]);
         if (STATES) continue;
-        ok = mbar_wait(&B.q_empty, (c & 1) ^ 1, D.err);
+        ok = wait_bar(&B.q_empty, c + 1, D.err);
         if (!ok) break;
         mbar_arrive_expect_tx(&B.q_full, QB);
 #pragma unroll
@@ -369,97 +429,117 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       if (!ok) B.failed = 1;
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp == DC_MMA) {
     // -------------------------------------------------------- products
     if (tc::elect_one()) {
       constexpr uint32_t id_p = tc::idesc_bf16(128, 128, false, false);
       constexpr uint32_t id_o = tc::idesc_bf16(128, 64, false, true);
-      constexpr uint32_t id_s = tc::idesc_bf16(128, 64, true, true);
-      const uint32_t b0 = smem_u32(base), v0 = smem_u32(vt), s0 = smem_u32(sb);
-      const uint32_t q = smem_u32(qb);
+      constexpr uint32_t id_s = tc::idesc_bf16(128, 192, true, true);
+      // descriptors count 16-byte units: 16 of a K-major operand's K are 2 of them (64 of
+      // K a block of 1024), 16 rows of an MN-major one 128
+      const uint64_t k_major = tc::desc_sw128(smem_u32(base), 16, 1024);
+      const uint64_t kt_desc = tc::desc_sw128(smem_u32(base), 16384, 1024);
+      const uint64_t v_desc = tc::desc_sw128(smem_u32(base) + QB, 8192, 1024);
+      const uint64_t q_desc = tc::desc_sw128(smem_u32(qb), 16, 1024);
+      const uint64_t s_desc = tc::desc_sw128(smem_u32(sb), 8192, 1024);
+      const uint64_t vt_desc = tc::desc_sw128(smem_u32(vt), VB, 1024);
       bool ok = true;
       auto scores = [&](int c) {  // Q Kᵀ
-        ok = mbar_wait(&B.q_full, c & 1, D.err) &&
-             mbar_wait(&B.full[c & 1], (c >> 1) & 1, D.err);
+        ok = wait_bar(&B.q_full, c, D.err) && wait_bar(&B.full[c & 1], c >> 1, D.err);
         if (!ok) return;
         tc::fence_after_sync();
-        const uint32_t k = b0 + (c & 1) * STAGE;
-#pragma unroll
+        const uint64_t k = k_major + (c & 1) * (STAGE / 16);
+#pragma unroll 2
         for (int kk = 0; kk < DK / 16; ++kk) {
-          const uint32_t at = 16384 * (kk >> 2) + 32 * (kk & 3);
-          tc::mma_bf16(tmem + T_P, tc::desc_sw128(q + at, 16, 1024),
-                       tc::desc_sw128(k + at, 16, 1024), id_p, kk > 0);
+          const int at = 1024 * (kk >> 2) + 2 * (kk & 3);
+          tc::mma_bf16(tmem + T_P, q_desc + at, k + at, id_p, kk > 0);
         }
         tc::commit(&B.p_full);
       };
-      if (!STATES) scores(0);
-      for (int c = 0; c < n && ok; ++c) {
-        const int s = c & 1, ph = (c >> 1) & 1;
-        const uint32_t k = b0 + s * STAGE, v = k + QB;
-        if (!STATES) {
+#pragma unroll 1
+      for (int c = STATES ? 0 : -1; c < n; ++c) {
+        const int s = c & 1;
+        const int stage = s * (STAGE / 16);
+        if (!STATES && c >= 0) {
           // Q S
-          ok = mbar_wait(&B.sb_full, c & 1, D.err) && mbar_wait(&B.o_empty[s], ph ^ 1, D.err);
+          ok = wait_bar(&B.sb_full, c, D.err) && wait_bar(&B.o_empty[s], (c >> 1) + 1, D.err);
           if (!ok) break;
           tc::fence_after_sync();
-#pragma unroll
+#pragma unroll 2
           for (int kk = 0; kk < DK / 16; ++kk)
-            tc::mma_bf16(tmem + T_O + 128 * s,
-                         tc::desc_sw128(q + 16384 * (kk >> 2) + 32 * (kk & 3), 16, 1024),
-                         tc::desc_sw128(s0 + 2048 * kk, 8192, 1024), id_o, kk > 0);
+            tc::mma_bf16(tmem + T_OS + 64 * s, q_desc + 1024 * (kk >> 2) + 2 * (kk & 3), s_desc + 128 * kk,
+                         id_o, kk > 0);
           tc::commit(&B.q_empty);
-        } else {
-          ok = mbar_wait(&B.full[s], ph, D.err);
+        }
+        if (c >= 0) {
+          if (STATES) {
+            ok = wait_bar(&B.full[s], c >> 1, D.err);
+            if (!ok) break;
+          }
+          // S += Kᵀ Ṽ, its three terms side by side (K is read once; with k_dim 64, lanes
+          // 64.. take v's rows for columns of k: never read)
+          ok = wait_bar(&B.vt_full, c, D.err);
+          if (!ok) break;
+          tc::fence_after_sync();
+          const uint64_t terms = vt_desc + (c & (NV - 1)) * (3 * VB / 16);
+#pragma unroll 2
+          for (int kk = 0; kk < CH / 16; ++kk)
+            tc::mma_bf16(tmem + T_S, kt_desc + stage + 128 * kk, terms + 128 * kk, id_s,
+                         !STATES || c > 0 || kk > 0);
+          if (STATES) {
+            tc::commit(&B.vt_empty[s]);
+            tc::commit(&B.empty[s]);
+            continue;
+          }
+          tc::commit(&B.s_full);
+          // the masked products times V
+          ok = wait_bar(&B.pt_full, c, D.err) &&
+               (c == 0 || wait_bar(&B.o_empty[s ^ 1], (c - 1) >> 1, D.err));
+          if (!ok) break;
+          tc::fence_after_sync();
+#pragma unroll 2
+          for (int kk = 0; kk < CH / 16; ++kk)
+            tc::mma_bf16_a_tmem(tmem + T_O, tmem + T_P + 32 * (kk >> 1) + 8 * (kk & 1),
+                                v_desc + stage + 128 * kk, id_o, kk > 0);
+          tc::commit(&B.o_full);
+          tc::commit(&B.empty[s]);
+        }
+        if (c + 1 < n) {
+          scores(c + 1);
           if (!ok) break;
         }
-        // S += Kᵀ Ṽ (with k_dim 64, lanes 64.. take v's rows for columns of k: never read)
-        ok = mbar_wait(&B.vt_full, c & 1, D.err);
-        if (!ok) break;
-        tc::fence_after_sync();
-#pragma unroll
-        for (int part = 0; part < 3; ++part)
-#pragma unroll
-          for (int kk = 0; kk < CH / 16; ++kk)
-            tc::mma_bf16(tmem + T_S, tc::desc_sw128(k + 2048 * kk, 16384, 1024),
-                         tc::desc_sw128(v0 + VB * (3 * (c & (NV - 1)) + part) + 2048 * kk, 8192, 1024),
-                         id_s, !STATES || c > 0 || part > 0 || kk > 0);
-        if (STATES) {
-          tc::commit(&B.vt_empty[s]);
-          tc::commit(&B.empty[s]);
-          continue;
-        }
-        tc::commit(&B.s_full);
-        // the masked products times V
-        ok = mbar_wait(&B.pt_full, c & 1, D.err);
-        if (!ok) break;
-        tc::fence_after_sync();
-#pragma unroll
-        for (int kk = 0; kk < CH / 16; ++kk)
-          tc::mma_bf16_a_tmem(tmem + T_O + 128 * s + 64, tmem + T_PT + 8 * kk,
-                              tc::desc_sw128(v + 2048 * kk, 8192, 1024), id_o, kk > 0);
-        tc::commit(&B.o_full[s]);
-        tc::commit(&B.pt_empty);
-        tc::commit(&B.empty[s]);
-        if (c + 1 < n) scores(c + 1);
       }
       if (!ok) B.failed = 1;
       if (STATES) tc::commit(&B.last);
       tc::commit(&B.done);
-      mbar_wait(&B.done, 0, D.err);  // nothing is on the tensor cores at exit
+      wait_bar(&B.done, 0, D.err);  // nothing is on the tensor cores at exit
     }
     __syncwarp();
-  } else if (warp == 2) {
+  } else if (warp == DC_GATES) {
     // ---------------------------------------------------------- decays
     constexpr double kLog2e = 1.4426950408889634;
+    const float log_scale = log2f(fabsf(D.scale));
     double R = 0.0;  // STATES: the decay behind the chunk
+    // the next chunk's log-decays are on their way while this one's are summed
+    float next[4];
+    auto fetch = [&](int c) {
+      const int t = it.t0 + CH * (STATES ? n - 1 - c : c) + 4 * lane;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) next[i] = t + i < it.t1 ? D.g[(t + i) * D.ldg + h] : 0.f;
+    };
+    fetch(0);
+#pragma unroll 1
     for (int c = 0; c < n; ++c) {
       const int t = it.t0 + CH * (STATES ? n - 1 - c : c) + 4 * lane;
+      float now[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) now[i] = next[i];
+      if (c + 1 < n) fetch(c + 1);
       double G[4];
-      bool up = false;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float g = t + i < it.t1 ? D.g[(t + i) * D.ldg + h] : 0.f;
-        up |= g > 0.f;
-        if (g < -1000.f) g = -1000.f;  // e^-1000 is 0, and -inf has no differences
+        float g = now[i];
+        if (g < -150.f) g = -150.f;  // e^-150 is 0 in FP32, and -inf has no differences
         G[i] = (double)g * kLog2e + (i ? G[i - 1] : 0.0);
       }
       double sum = G[3];
@@ -470,27 +550,23 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       }
       const double front = sum - G[3], total = __shfl_sync(0xffffffffu, sum, 31);
       const double first = front + G[0], own = __shfl_sync(0xffffffffu, first, lane & ~7);
-      double later[3];  // G at the first rows of blocks 1, 2, 3
+      double later[4];  // G at the blocks' first rows
 #pragma unroll
-      for (int q = 1; q < 4; ++q) later[q - 1] = __shfl_sync(0xffffffffu, first, 8 * q);
-      up = __any_sync(0xffffffffu, up);
+      for (int q = 0; q < 4; ++q) later[q] = __shfl_sync(0xffffffffu, first, 8 * q);
       if (!wait(&B.gate_empty[c & 1], ((c >> 1) & 1) ^ 1)) break;
       Gates& g = B.gate[c & 1];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const double x = front + G[i];
-        const float hi = (float)x;
-        g.hi[4 * lane + i] = hi;
-        g.lo[4 * lane + i] = (float)(x - (double)hi);
-        g.w[4 * lane + i] = t + i < it.t1 ? exp2f((float)(R + (total - x))) : 0.f;
+        g.w[4 * lane + i] = t + i < it.t1 ? ex2((float)(R + (total - x))) : 0.f;
         if (STATES) continue;
-        g.e[4 * lane + i] = D.scale * exp2f(hi);
-        g.rf[4 * lane + i] = ex2((float)(x - own));
+        g.e[4 * lane + i] = fabsf(D.scale) * ex2((float)x);
+        g.row[4 * lane + i] = (float)(x - own) + log_scale;
 #pragma unroll
-        for (int q = 1; q < 4; ++q)
-          if (lane < 8 * q) g.cf[16 * q * (q - 1) + 4 * lane + i] = ex2((float)(later[q - 1] - x));
+        for (int q = 0; q < 4; ++q)
+          if (lane < 8 * q + 8) g.col[col_at(q) + 4 * lane + i] = (float)(later[q] - x);
       }
-      if (lane == 0) g.tot = exp2f((float)total), g.grow = up;
+      if (lane == 0) g.tot = ex2((float)total);
       if (STATES) {
         R += total;
         if (lane == 0) B.g_total = R;
@@ -498,58 +574,40 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       arrive(&B.gate_full[c & 1]);
     }
     if (STATES && lane == 0 && c0 == 0) P.Wg[(size_t)(it.slot + it.seg) * D.HV + h] = R;
-  } else if (warp >= 4 && warp < 12) {
-    // ----------------------------------------------- Q Kᵀ's rows, masked
-    if (!STATES) {
-      const int quad = warp & 3, half = (warp - 4) >> 2;
+  } else if (warp < 16) {
+    // ------------------------- a block of Q Kᵀ, decayed and masked, to BF16
+    const int quad = warp & 3, cb = warp >> 2, y = 32 * cb;
+    if (!STATES && cb <= quad) {
       const uint32_t lanes = (uint32_t)(32 * quad) << 16;
       const int i = 32 * quad + lane;
-      // columns right of the diagonal block stay zero
-      uint32_t z[16] = {};
-      for (int cb = half; cb < 4; cb += 2) tc::tmem_st16(tmem + lanes + T_PT + 16 * cb, z);
+#pragma unroll 1
       for (int c = 0; c < n; ++c) {
-        if (!wait(&B.p_full, c) || !wait(&B.gate_full[c & 1], c >> 1) ||
-            !wait(&B.pt_empty, c + 1))
-          break;
+        if (!wait(&B.gate_full[c & 1], c >> 1) || !wait(&B.p_full, c)) break;
         tc::fence_after_sync();
         const Gates& g = B.gate[c & 1];
-        const bool factors = !g.grow;
+        uint32_t r[32], o[16];
+        tc::tmem_ld32(tmem + lanes + T_P + y, r);
+        tc::tmem_wait_ld();
+        // a column right of the diagonal is masked, whatever it holds
+        const float row = g.row[i];
+        const float* col = &g.col[col_at(quad) + y];
+        const int last = i - y;
+#pragma unroll
+        for (int x = 0; x < 32; x += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(col + x);
+          const float p0 = __uint_as_float(r[x]) * ex2(row + f.x);
+          const float p1 = __uint_as_float(r[x + 1]) * ex2(row + f.y);
+          const float p2 = __uint_as_float(r[x + 2]) * ex2(row + f.z);
+          const float p3 = __uint_as_float(r[x + 3]) * ex2(row + f.w);
+          o[x / 2] = pack2_bf(x <= last ? p0 : 0.f, x + 1 <= last ? p1 : 0.f);
+          o[x / 2 + 1] = pack2_bf(x + 2 <= last ? p2 : 0.f, x + 3 <= last ? p3 : 0.f);
+        }
+        tc::tmem_st16(tmem + lanes + T_P + y, o);
+        if (cb == quad) {
+          // the blocks right of the diagonal one
+          const uint32_t z[16] = {};
 #pragma unroll 1
-        for (int cb = half; cb <= quad; cb += 2) {
-          uint32_t r[32];
-          tc::tmem_ld32(tmem + lanes + T_P + 32 * cb, r);
-          tc::tmem_wait_ld();
-          if (cb < quad && factors) {
-            const float rf = g.rf[i];
-            const float* cf = &g.cf[16 * quad * (quad - 1) + 32 * cb];
-#pragma unroll
-            for (int x = 0; x < 32; x += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(cf + x);
-              r[x / 2] = pack2_bf(__uint_as_float(r[x]) * (rf * f.x),
-                                  __uint_as_float(r[x + 1]) * (rf * f.y));
-              r[x / 2 + 1] = pack2_bf(__uint_as_float(r[x + 2]) * (rf * f.z),
-                                      __uint_as_float(r[x + 3]) * (rf * f.w));
-            }
-          } else {
-            // a column right of the diagonal is masked, whatever it holds
-            const float hi = g.hi[i], lo = g.lo[i];
-            const int last = cb == quad ? lane : 31;
-#pragma unroll
-            for (int x = 0; x < 32; x += 4) {
-              const float4 gh = *reinterpret_cast<const float4*>(&g.hi[32 * cb + x]);
-              const float4 gl = *reinterpret_cast<const float4*>(&g.lo[32 * cb + x]);
-              const float p0 = __uint_as_float(r[x]) * ex2((hi - gh.x) + (lo - gl.x));
-              const float p1 = __uint_as_float(r[x + 1]) * ex2((hi - gh.y) + (lo - gl.y));
-              const float p2 = __uint_as_float(r[x + 2]) * ex2((hi - gh.z) + (lo - gl.z));
-              const float p3 = __uint_as_float(r[x + 3]) * ex2((hi - gh.w) + (lo - gl.w));
-              r[x / 2] = pack2_bf(x <= last ? p0 : 0.f, x + 1 <= last ? p1 : 0.f);
-              r[x / 2 + 1] = pack2_bf(x + 2 <= last ? p2 : 0.f, x + 3 <= last ? p3 : 0.f);
-            }
-          }
-          uint32_t o[16];
-#pragma unroll
-          for (int x = 0; x < 16; ++x) o[x] = r[x];
-          tc::tmem_st16(tmem + lanes + T_PT + 16 * cb, o);
+          for (int x = y + 32; x < CH; x += 32) tc::tmem_st16(tmem + lanes + T_P + x, z);
         }
         tc::tmem_wait_st();
         tc::fence_before_sync();
@@ -557,12 +615,14 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         if (lane == 0) mbar_arrive(&B.gate_empty[c & 1]);
       }
     }
-  } else if (warp >= 12 && warp < 20) {
+  } else if (warp < 24) {
     // ------------------------------- Ṽ, then o: 32 columns of a row a thread
-    const int quad = warp & 3, half = (warp - 12) >> 2, j = 32 * quad + lane;
+    const int quad = warp & 3, half = (warp - 16) >> 2, j = 32 * quad + lane;
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
-    const int tid = threadIdx.x - 32 * 12;
+    const int tid = threadIdx.x - 32 * 16;
+    const uint32_t sign = D.scale < 0.f ? 0x80008000u : 0u;
     float e = 0.f;
+#pragma unroll 1
     for (int c = 0; c <= n; ++c) {
       const float e_prev = e;
       if (c < n) {
@@ -572,123 +632,124 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
           if (tid == 64) B.anybad[c & 3] = 0;
           named_bar_sync(1, 256);
         }
-        if (!wait(&B.full[s], c >> 1) || !wait(&B.gate_full[s], c >> 1) ||
-            !(STATES ? wait(&B.vt_empty[s], (c >> 1) + 1) : c == 0 || wait(&B.s_full, c - 1)))
-          break;
+        if (!wait(&B.full[s], c >> 1) || !wait(&B.gate_full[s], c >> 1)) break;
         const float w = B.gate[s].w[j];
         if (!STATES) e = B.gate[s].e[j];
         unsigned char* st = base + s * STAGE;
         unsigned char* v = st + QB + 128 * j;
         unsigned char* to = vt + 3 * VB * (c & (NV - 1)) + 128 * j;
         const int sw = j & 7;
-        if (t < it.t1) {
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const int x = 4 * half + y, at = 16 * (x ^ sw);
-            const uint4 word = *reinterpret_cast<const uint4*>(v + at);
-            uint32_t in[4] = {word.x, word.y, word.z, word.w}, hi[4], mid[4], lo[4];
-            float odd = 0.f;  // NaN once a value of v is infinite or NaN
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              float a = bf_lo(in[m]), b = bf_hi(in[m]);
-              odd = fmaf(a, 0.f, fmaf(b, 0.f, odd));
-              a *= w, b *= w;
-              hi[m] = pack2_bf(a, b);
-              a -= bf_lo(hi[m]), b -= bf_hi(hi[m]);
-              mid[m] = pack2_bf(a, b);
-              lo[m] = pack2_bf(a - bf_lo(mid[m]), b - bf_hi(mid[m]));
-            }
-            if (odd != 0.f) {
-#pragma unroll
-              for (int m = 0; m < 4; ++m) {
-                if ((in[m] & 0x7F80u) == 0x7F80u) {
-                  if (!STATES) atomicMin(&B.colbad[c & 3][8 * x + 2 * m], j);
-                  in[m] &= 0xFFFF0000u;
-                  hi[m] |= 0x7FFFu;
-                }
-                if ((in[m] & 0x7F800000u) == 0x7F800000u) {
-                  if (!STATES) atomicMin(&B.colbad[c & 3][8 * x + 2 * m + 1], j);
-                  in[m] &= 0x0000FFFFu;
-                  hi[m] |= 0x7FFF0000u;
-                }
-              }
-              B.anybad[c & 3] = 1;
-              *reinterpret_cast<uint4*>(v + at) = make_uint4(in[0], in[1], in[2], in[3]);
-            }
-            *reinterpret_cast<uint4*>(to + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(to + VB + at) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-            *reinterpret_cast<uint4*>(to + 2 * VB + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          }
-        } else {
-          // behind the sequence: another one's rows, or nothing
-          const uint4 z = make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const int at = 16 * (4 * half + y);
-            *reinterpret_cast<uint4*>(v + at) = z;
-#pragma unroll
-            for (int part = 0; part < 3; ++part)
-              *reinterpret_cast<uint4*>(to + part * VB + at) = z;
+        if (!(STATES ? wait(&B.vt_empty[s], (c >> 1) + 1) : c == 0 || wait(&B.s_full, c - 1)))
+          break;
+        uint32_t odd = 0;  // NaN (in either half) once a value of v is infinite or NaN
+#pragma unroll 2
+        for (int y = 0; y < 4; ++y) {
+          const int at = 16 * ((4 * half + y) ^ sw);
+          uint4 word = make_uint4(0, 0, 0, 0);
+          if (t < it.t1) {
+            word = *reinterpret_cast<const uint4*>(v + at);
+          } else {
+            // behind the sequence: another one's rows, or nothing
+            *reinterpret_cast<uint4*>(v + at) = word;
 #pragma unroll
             for (int x = 0; x < DK / 64; ++x)
-              *reinterpret_cast<uint4*>(st + 16384 * x + 128 * j + at) = z;
+              *reinterpret_cast<uint4*>(st + 16384 * x + 128 * j + at) = word;
           }
+          const uint32_t in[4] = {word.x, word.y, word.z, word.w};
+          uint32_t hi[4], mid[4], lo[4];
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            float a = bf_lo(in[m]), b = bf_hi(in[m]);
+            odd = times_zero(in[m], odd);
+            a *= w, b *= w;
+            hi[m] = pack2_bf(a, b);
+            a -= bf_lo(hi[m]), b -= bf_hi(hi[m]);
+            mid[m] = pack2_bf(a, b);
+            lo[m] = pack2_bf(a - bf_lo(mid[m]), b - bf_hi(mid[m]));
+          }
+          *reinterpret_cast<uint4*>(to + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(to + VB + at) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+          *reinterpret_cast<uint4*>(to + 2 * VB + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
+        if (odd & 0x7FFF7FFFu) mark_row(v, to, sw, half, j, B.colbad[c & 3], &B.anybad[c & 3]);
         tc::fence_async_smem();
         arrive(&B.vt_full);
         if (lane == 0) mbar_arrive(&B.gate_empty[s]);
       }
       if (!STATES && c > 0) {
-        const int cc = c - 1, s = cc & 1, t = it.t0 + CH * cc + j;
+        const int cc = c - 1, t = it.t0 + CH * cc + j;
         if (c == n) named_bar_sync(1, 256);  // the last chunk's marks
-        if (!wait(&B.o_full[s], cc >> 1)) break;
+        if (!wait(&B.o_full, cc)) break;
         tc::fence_after_sync();
         const int col = 32 * half;
+        // whole blocks of 32 rows go out by TMA from a warp's own 2 KB (16-byte chunk x of
+        // row l at x ^ l / 2 % 4), the last ones of a sequence by plain stores
+        unsigned char* mine = ob + 2048 * (warp - 16);
+        const bool whole = t - lane + 32 <= it.t1;
         uint16_t* o = D.o + t * D.ldo + h * D.DV + c0 + col;
-        const bool marks = B.anybad[cc & 3] != 0;
-#pragma unroll
-        for (int cb = 0; cb < 2; ++cb) {
+        if (lane == 0) tc::bulk_wait_read<0>();
+        __syncwarp();
+#pragma unroll 1
+        for (int y = 0; y < 32; y += 16) {
           uint32_t a[16], b[16];
-          tc::tmem_ld16(tmem + lanes + T_O + 128 * s + col + 16 * cb, a);
-          tc::tmem_ld16(tmem + lanes + T_O + 128 * s + 64 + col + 16 * cb, b);
+          tc::tmem_ld16(tmem + lanes + T_OS + 64 * (cc & 1) + col + y, a);
+          tc::tmem_ld16(tmem + lanes + T_O + col + y, b);
           tc::tmem_wait_ld();
-          if (cb == 1) {
-            tc::fence_before_sync();
-            arrive(&B.o_empty[s]);
-          }
-          if (t >= it.t1) continue;
-          uint32_t y[8];
+          uint32_t z[8];
 #pragma unroll
           for (int m = 0; m < 8; ++m)
-            y[m] = pack2_bf(
-                fmaf(e_prev, __uint_as_float(a[2 * m]), D.scale * __uint_as_float(b[2 * m])),
-                fmaf(e_prev, __uint_as_float(a[2 * m + 1]),
-                     D.scale * __uint_as_float(b[2 * m + 1])));
-          if (marks) {
-#pragma unroll
-            for (int m = 0; m < 8; ++m) {
-              const int u = col + 16 * cb + 2 * m;
-              if (B.colbad[cc & 3][u] <= j) y[m] |= 0x7FFFu;
-              if (B.colbad[cc & 3][u + 1] <= j) y[m] |= 0x7FFF0000u;
-            }
+            z[m] = sign ^ pack2_bf(fmaf(e_prev, __uint_as_float(a[2 * m]), __uint_as_float(b[2 * m])),
+                                   fmaf(e_prev, __uint_as_float(a[2 * m + 1]),
+                                        __uint_as_float(b[2 * m + 1])));
+          const int x = y / 8;
+          if (whole) {
+            unsigned char* l = mine + 64 * lane;
+            const int sw = (lane >> 1) & 3;
+            *reinterpret_cast<uint4*>(l + 16 * (x ^ sw)) = make_uint4(z[0], z[1], z[2], z[3]);
+            *reinterpret_cast<uint4*>(l + 16 * ((x + 1) ^ sw)) =
+                make_uint4(z[4], z[5], z[6], z[7]);
+          } else if (t < it.t1) {
+            *reinterpret_cast<uint4*>(o + y) = make_uint4(z[0], z[1], z[2], z[3]);
+            *reinterpret_cast<uint4*>(o + y + 8) = make_uint4(z[4], z[5], z[6], z[7]);
           }
-          *reinterpret_cast<uint4*>(o + 16 * cb) = make_uint4(y[0], y[1], y[2], y[3]);
-          *reinterpret_cast<uint4*>(o + 16 * cb + 8) = make_uint4(y[4], y[5], y[6], y[7]);
+        }
+        tc::fence_before_sync();
+        arrive(&B.o_empty[cc & 1]);
+        if (B.anybad[cc & 3]) {
+          // a column is NaN from its first marked token on
+#pragma unroll 1
+          for (int u = 0; u < 32; ++u)
+            if (B.colbad[cc & 3][col + u] <= j) {
+              if (whole)
+                reinterpret_cast<uint16_t*>(mine + 64 * lane +
+                                            16 * ((u / 8) ^ ((lane >> 1) & 3)))[u & 7] = 0x7FFF;
+              else if (t < it.t1)
+                o[u] = 0x7FFF;
+            }
+        }
+        if (whole) {
+          tc::fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tc::tma_store_2d(&P.o_map, D.DV * h + c0 + col, t, mine);
+            tc::bulk_commit();
+          }
         }
       }
     }
-  } else if (warp >= 20) {
+    if (!STATES && lane == 0) tc::bulk_wait_all();
+  } else {
     // ------------------------------------------------------- the state
     const int quad = warp & 3, d = 32 * quad + lane;
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
     const bool mine = 32 * quad < DK;
     float* row = D.state + (((size_t)it.row * D.HV + h) * DK + d) * D.DV + c0;
     const float* left = W0 + (size_t)d * D.DV + c0;  // what segment 0 leaves behind
-    // 32 columns at a time; `x` of the functions below is their first column
-    float S[32];
+    // 16 columns at a time; `x` of the functions below is their first column
+    float S[16];
     auto load = [&](const float* from, float f) {
 #pragma unroll
-      for (int i = 0; i < 32; i += 4) {
+      for (int i = 0; i < 16; i += 4) {
         const float4 y = *reinterpret_cast<const float4*>(from + i);
         S[i] = fmaf(f, y.x, S[i]), S[i + 1] = fmaf(f, y.y, S[i + 1]);
         S[i + 2] = fmaf(f, y.z, S[i + 2]), S[i + 3] = fmaf(f, y.w, S[i + 3]);
@@ -696,30 +757,35 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     };
     auto clear = [&]() {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) S[i] = 0.f;
+      for (int i = 0; i < 16; ++i) S[i] = 0.f;
     };
     // what the first `segs` segments leave behind, together
     auto join = [&](int x, int segs) {
       clear();
       double R = 0.0;
+#pragma unroll 1
       for (int g = segs - 1; g >= 0; --g) {
-        load(left + (size_t)g * D.HV * plane + x, exp2f((float)R));
+        load(left + (size_t)g * D.HV * plane + x, ex2((float)R));
         R += P.Wg[(size_t)(it.slot + g) * D.HV + h];
       }
     };
     auto from_tmem = [&](int x) {
-      uint32_t r[32];
-      tc::tmem_ld32(tmem + lanes + T_S + x, r);
+      uint32_t hi[16], mid[16], lo[16];
+      tc::tmem_ld16(tmem + lanes + T_S + x, hi);
+      tc::tmem_ld16(tmem + lanes + T_S + 64 + x, mid);
+      tc::tmem_ld16(tmem + lanes + T_S + 128 + x, lo);
       tc::tmem_wait_ld();
 #pragma unroll
-      for (int i = 0; i < 32; ++i) S[i] = __uint_as_float(r[i]);
+      for (int i = 0; i < 16; ++i)
+        S[i] = __uint_as_float(hi[i]) + (__uint_as_float(mid[i]) + __uint_as_float(lo[i]));
     };
     auto store = [&](float* to) {
 #pragma unroll
-      for (int i = 0; i < 32; i += 4)
+      for (int i = 0; i < 16; i += 4)
         *reinterpret_cast<float4*>(to + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
     };
     bool ok = true;
+#pragma unroll 1
     for (int c = 0; !STATES && c < n; ++c) {
       if (c > 0) {
         ok = wait(&B.s_full, c - 1);
@@ -730,8 +796,9 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       if (!ok) break;
       if (mine) {
         const float tot = B.gate[c & 1].tot;
+        const uint32_t zero[16] = {};
 #pragma unroll 1
-        for (int x = 0; x < 64; x += 32) {
+        for (int x = 0; x < 64; x += 16) {
           if (c > 0) {
             from_tmem(x);
           } else if (it.seg == 0) {
@@ -741,14 +808,16 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
             join(x, it.seg);
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 2; ++i)
             *reinterpret_cast<uint4*>(sb + 128 * d + 16 * ((x / 8 + i) ^ (d & 7))) = make_uint4(
                 pack2_bf(S[8 * i], S[8 * i + 1]), pack2_bf(S[8 * i + 2], S[8 * i + 3]),
                 pack2_bf(S[8 * i + 4], S[8 * i + 5]), pack2_bf(S[8 * i + 6], S[8 * i + 7]));
-          uint32_t r[32];
+          uint32_t r[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(S[i] * tot);
-          tc::tmem_st32(tmem + lanes + T_S + x, r);
+          for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(S[i] * tot);
+          tc::tmem_st16(tmem + lanes + T_S + x, r);
+          tc::tmem_st16(tmem + lanes + T_S + 64 + x, zero);
+          tc::tmem_st16(tmem + lanes + T_S + 128 + x, zero);
         }
         tc::tmem_wait_st();
       }
@@ -762,10 +831,10 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     if (ok && mine && !B.failed) {
       tc::fence_after_sync();
 #pragma unroll 1
-      for (int x = 0; x < 64; x += 32) {
+      for (int x = 0; x < 64; x += 16) {
         if (STATES) {
           from_tmem(x);
-          if (it.seg == 0) load(row + x, exp2f((float)B.g_total));
+          if (it.seg == 0) load(row + x, ex2((float)B.g_total));
           store(const_cast<float*>(left) + (size_t)it.seg * D.HV * plane + x);
         } else if (it.nseg == 1) {
           from_tmem(x);
@@ -786,16 +855,17 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     while (globaltimer_ns() - tw < kDrainNs) {
     }
   }
-  if (warp == 1) {
+  if (warp == DC_MMA) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, 512);
   }
 }
 
-// k, v twice; three terms of Ṽ, q and S (twice the terms for STATES); the rest, alignment.
+// k, v twice; three terms of Ṽ, q, S and o (twice the terms for STATES); the rest,
+// alignment.
 constexpr int chunk_smem(int DK) {
   constexpr int terms = 3 * 16384;
-  const int main = terms + 256 * DK + 128 * DK;
+  const int main = terms + 256 * DK + 128 * DK + 16384;
   return 2 * (256 * DK + 16384) + (main > 2 * terms ? main : 2 * terms) + 10240;
 }
 
@@ -845,7 +915,8 @@ int launch_prefill(const DecayParams& D, void* ws, cudaStream_t st) {
   prefill_bytes(D.T, D.HV, D.DK, D.DV, &P.W, &P.Wg, ws);
   if (!encode_rows(&P.q_map, D.q, false, D.HK * D.DK, D.T, D.ldq * 2, 64, CH) ||
       !encode_rows(&P.k_map, D.k, false, D.HK * D.DK, D.T, D.ldk * 2, 64, CH) ||
-      !encode_rows(&P.v_map, D.v, false, D.HV * D.DV, D.T, D.ldv * 2, 64, CH))
+      !encode_rows(&P.v_map, D.v, false, D.HV * D.DV, D.T, D.ldv * 2, 64, CH) ||
+      !encode_rows(&P.o_map, D.o, false, D.HV * D.DV, D.T, D.ldo * 2, 32, 32))
     return ER_ECUDA;
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -155,6 +155,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
+// The same with 8 columns.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -406,8 +414,8 @@ bool encode_store_2d(CUtensorMap* m, const void* base, bool fp32, uint64_t cols,
 bool encode_bf16_2d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows,
                     uint64_t pitch_bytes, uint32_t box_cols, uint32_t box_rows);
 
-// Host: the same for BF16 or FP32 rows, loads and stores with 128-byte swizzle,
-// encoded anew by every call.
+// Host: the same for BF16 or FP32 rows, loads and stores, 128-byte swizzle (64-byte for
+// box rows of 64 bytes), encoded anew by every call.
 bool encode_rows(CUtensorMap* m, const void* base, bool fp32, uint64_t cols, uint64_t rows,
                  uint64_t pitch_bytes, uint32_t box_cols, uint32_t box_rows);
 

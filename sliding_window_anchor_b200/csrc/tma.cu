@@ -151,7 +151,7 @@ bool encode_store_2d(CUtensorMap* m, const void* base, bool fp32, uint64_t cols,
 
 // Host: a 2-D map over `rows` rows of `cols` BF16 or FP32 elements, row pitch
 // `pitch_bytes`, boxes of box_cols x box_rows with 128-byte swizzle (a box row is at
-// most 128 bytes), for loads (zero outside the matrix) and stores (nothing
+// most 128 bytes; 64-byte swizzle for rows of 64), for loads (zero outside the matrix) and stores (nothing
 // outside).  Encoded anew by every call.
 bool encode_rows(CUtensorMap* m, const void* base, bool fp32, uint64_t cols, uint64_t rows,
                  uint64_t pitch_bytes, uint32_t box_cols, uint32_t box_rows) {
@@ -164,7 +164,8 @@ bool encode_rows(CUtensorMap* m, const void* base, bool fp32, uint64_t cols, uin
   const cuuint32_t estr[2] = {1, 1};
   return fn(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            box_cols * (fp32 ? 4 : 2) == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
