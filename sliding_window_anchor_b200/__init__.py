@@ -242,13 +242,6 @@ def linear(x: torch.Tensor, w: torch.Tensor, fp32_out: bool = False, out=None, w
     return out
 
 
-def _device_of(x: torch.Tensor, name: str):
-    """The device of a call's tensors (that of its first one)."""
-    if not x.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return x.device
-
-
 def _on_stream(f):
     """`stream=`: run the call with that stream as the current one, so that what it
     allocates belongs to the stream that uses it."""
@@ -263,34 +256,57 @@ def _on_stream(f):
     return g
 
 
+# The current device and a device's current stream as numbers (torch.cuda's functions of
+# these names take 4 us a call to build their objects, half of a small call's time).
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else None
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+if _current_device is None or _raw_stream is None:  # a torch built without them
+    def _current_device():
+        return torch.cuda.current_device()
+
+    def _raw_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
+
+
+def _device_of(x: torch.Tensor, name: str):
+    """The device of a call's tensors (that of its first one)."""
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return x.device
+
+
 def _call(fn: str, device, *args):
     """Call a C entry point on its tensors' device and that device's current stream."""
-    f = getattr(lib(), fn)
-    s = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
-        rc = f(*args, s)
+    f = getattr(_lib._lib or lib(), fn)
+    index = device.index
+    if _current_device() == index:
+        rc = f(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            rc = f(*args, s)
+            rc = f(*args, _raw_stream(index))
     if rc != 0:
         raise ERError(fn, rc)
+
+
+def _wrong(t, device, dtype, shape, name):
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _arg(t, device, dtype, shape, name):
     """The address of a tensor whose last dimensions are dense and whose rows
     (dimension 0) may be strided, and that row stride in elements."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        _wrong(t, device, dtype, shape, name)
     st = t.stride()
     dense = 1
-    for n, d in zip(reversed(shape[1:]), reversed(st[1:])):
-        if d != dense and n != 1:
+    for i in range(len(shape) - 1, 0, -1):
+        if st[i] != dense and shape[i] != 1:
             raise ValueError(f"{name} must have dense rows, got strides {st}")
-        dense *= n
+        dense *= shape[i]
     # a single row's stride says nothing
     ld = st[0] if shape[0] > 1 else dense
     if ld < dense:
@@ -299,12 +315,8 @@ def _arg(t, device, dtype, shape, name):
 
 
 def _dense(t, device, dtype, shape, name):
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        _wrong(t, device, dtype, shape, name)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
