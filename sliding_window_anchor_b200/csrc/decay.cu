@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     k_decay_chunks(const __grid_constant__ ChunkParams P) {
   constexpr int QB = DK * 256;  // bytes of a chunk's q (or k) rows: 64-column blocks of 16 KB
   constexpr int VB = 16384;
-  constexpr int STAGE = QB + VB;        // k, v
+  constexpr int RV = STATES ? 3 : 2;    // chunks of v in flight (of k two)
   constexpr int NV = STATES ? 2 : 1;    // buffers of Ṽ
   // TMEM columns: Q Kᵀ, and that masked, as BF16, in the first 16 columns of each 32; the
   // state's sums, one for each term of Ṽ; the masked products times V; Q S, twice
@@ -325,7 +325,8 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  unsigned char* vt = base + 2 * STAGE;     // Ṽ: three terms
+  unsigned char* vb = base + 2 * QB;
+  unsigned char* vt = vb + RV * VB;         // Ṽ: three terms
   unsigned char* qb = vt + 3 * NV * VB;     // q
   unsigned char* sb = qb + (STATES ? 0 : QB);  // S in BF16, [DK][64]
   unsigned char* ob = sb + (STATES ? 0 : DK * 128);  // o on its way out
@@ -333,7 +334,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     Gates gate[2];
     int colbad[4][64];  // first token of a chunk with a non-finite v, by column
     int anybad[4];
-    uint64_t full[2], empty[2], gate_full[2], gate_empty[2];
+    uint64_t k_full[2], k_empty[2], v_full[3], v_empty[3], gate_full[2], gate_empty[2];
     uint64_t vt_empty[2], last;  // STATES
     uint64_t o_full, o_empty[2], q_full, q_empty, p_full, pt_full, vt_full, s_full, sb_full, done;
     double g_total;
@@ -353,11 +354,15 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   if (warp == 0) find_item(D, P.L, blockIdx.x / per, &B.item);
   if (threadIdx.x == 32) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&B.full[i], 1);
-      mbar_init(&B.empty[i], 1);
+      mbar_init(&B.k_full[i], 1);
+      mbar_init(&B.k_empty[i], 1);
       mbar_init(&B.gate_full[i], 1);
       mbar_init(&B.gate_empty[i], STATES ? 8 : 22);
       mbar_init(&B.vt_empty[i], 1);
+    }
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&B.v_full[i], 1);
+      mbar_init(&B.v_empty[i], STATES ? 8 : 1);
     }
     mbar_init(&B.last, 1);
     mbar_init(&B.o_full, 1);
@@ -383,14 +388,25 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     if (threadIdx.x == 0) set_dev_error(D.err, ER_EINVAL);
     return;
   }
+  const size_t plane = (size_t)DK * D.DV;
+  float* W0 = P.W + ((size_t)it.slot * D.HV + h) * plane;
+  if (STATES && it.seg == it.nseg - 1) {
+    // the last segment's walk writes the state's row, which the first one starts from: a
+    // copy of it for that one takes the slot that no later segment needs
+    const float* from = D.state + ((size_t)it.row * D.HV + h) * plane + c0;
+    float* to = W0 + (size_t)it.seg * D.HV * plane + c0;
+    for (int i = threadIdx.x; i < DK * 16; i += DC_THREADS) {
+      const size_t at = (size_t)(i / 16) * D.DV + 4 * (i % 16);
+      *reinterpret_cast<float4*>(to + at) = *reinterpret_cast<const float4*>(from + at);
+    }
+    return;
+  }
   if (warp == DC_MMA) tc::tmem_alloc(&B.tmem_base, 512);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = B.tmem_base;
   const int n = (it.t1 - it.t0 + CH - 1) / CH;
-  const size_t plane = (size_t)DK * D.DV;
-  const float* W0 = P.W + ((size_t)it.slot * D.HV + h) * plane;
 
   // a wait of a whole warp: false (in every lane) when it gave up or another one did
   auto wait = [&](uint64_t* bar, int phase) {
@@ -407,17 +423,26 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     // ------------------------------------------------------------- TMA
     if (tc::elect_one()) {
       bool ok = true;
+      int vs = 0, vp = 1;  // v's slot and phase
+      auto first_row = [&](int c) { return it.t0 + CH * (STATES ? n - 1 - c : c); };
+      auto load_v = [&](int c) {
+        ok = wait_bar(&B.v_empty[vs], vp, D.err);
+        if (!ok) return;
+        mbar_arrive_expect_tx(&B.v_full[vs], VB);
+        tc::tma_load_2d(vb + vs * VB, &P.v_map, D.DV * h + c0, first_row(c), &B.v_full[vs]);
+        if (++vs == RV) vs = 0, vp ^= 1;
+      };
+      load_v(0);
 #pragma unroll 1
-      for (int c = 0; c < n; ++c) {
-        const int s = c & 1, t = it.t0 + CH * (STATES ? n - 1 - c : c);
-        ok = wait_bar(&B.empty[s], (c >> 1) + 1, D.err);
+      for (int c = 0; ok && c < n; ++c) {
+        const int s = c & 1, t = first_row(c);
+        if (STATES && c + 1 < n) load_v(c + 1);
+        ok = ok && wait_bar(&B.k_empty[s], (c >> 1) + 1, D.err);
         if (!ok) break;
-        unsigned char* st = base + s * STAGE;
-        mbar_arrive_expect_tx(&B.full[s], STAGE);
+        mbar_arrive_expect_tx(&B.k_full[s], QB);
 #pragma unroll
         for (int x = 0; x < DK / 64; ++x)
-          tc::tma_load_2d(st + 16384 * x, &P.k_map, DK * hk + 64 * x, t, &B.full[s]);
-        tc::tma_load_2d(st + QB, &P.v_map, D.DV * h + c0, t, &B.full[s]);
+          tc::tma_load_2d(base + s * QB + 16384 * x, &P.k_map, DK * hk + 64 * x, t, &B.k_full[s]);
         if (STATES) continue;
         ok = wait_bar(&B.q_empty, c + 1, D.err);
         if (!ok) break;
@@ -425,6 +450,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
 #pragma unroll
         for (int x = 0; x < DK / 64; ++x)
           tc::tma_load_2d(qb + 16384 * x, &P.q_map, DK * hk + 64 * x, t, &B.q_full);
+        if (c + 1 < n) load_v(c + 1);
       }
       if (!ok) B.failed = 1;
     }
@@ -439,16 +465,16 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       // K a block of 1024), 16 rows of an MN-major one 128
       const uint64_t k_major = tc::desc_sw128(smem_u32(base), 16, 1024);
       const uint64_t kt_desc = tc::desc_sw128(smem_u32(base), 16384, 1024);
-      const uint64_t v_desc = tc::desc_sw128(smem_u32(base) + QB, 8192, 1024);
+      const uint64_t v_desc = tc::desc_sw128(smem_u32(vb), 8192, 1024);
       const uint64_t q_desc = tc::desc_sw128(smem_u32(qb), 16, 1024);
       const uint64_t s_desc = tc::desc_sw128(smem_u32(sb), 8192, 1024);
       const uint64_t vt_desc = tc::desc_sw128(smem_u32(vt), VB, 1024);
       bool ok = true;
       auto scores = [&](int c) {  // Q Kᵀ
-        ok = wait_bar(&B.q_full, c, D.err) && wait_bar(&B.full[c & 1], c >> 1, D.err);
+        ok = wait_bar(&B.q_full, c, D.err) && wait_bar(&B.k_full[c & 1], c >> 1, D.err);
         if (!ok) return;
         tc::fence_after_sync();
-        const uint64_t k = k_major + (c & 1) * (STAGE / 16);
+        const uint64_t k = k_major + (c & 1) * (QB / 16);
 #pragma unroll 2
         for (int kk = 0; kk < DK / 16; ++kk) {
           const int at = 1024 * (kk >> 2) + 2 * (kk & 3);
@@ -459,7 +485,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
 #pragma unroll 1
       for (int c = STATES ? 0 : -1; c < n; ++c) {
         const int s = c & 1;
-        const int stage = s * (STAGE / 16);
+        const int k_at = s * (QB / 16), v_at = s * (VB / 16);
         if (!STATES && c >= 0) {
           // Q S
           ok = wait_bar(&B.sb_full, c, D.err) && wait_bar(&B.o_empty[s], (c >> 1) + 1, D.err);
@@ -473,7 +499,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         }
         if (c >= 0) {
           if (STATES) {
-            ok = wait_bar(&B.full[s], c >> 1, D.err);
+            ok = wait_bar(&B.k_full[s], c >> 1, D.err);
             if (!ok) break;
           }
           // S += Kᵀ Ṽ, its three terms side by side (K is read once; with k_dim 64, lanes
@@ -484,14 +510,15 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
           const uint64_t terms = vt_desc + (c & (NV - 1)) * (3 * VB / 16);
 #pragma unroll 2
           for (int kk = 0; kk < CH / 16; ++kk)
-            tc::mma_bf16(tmem + T_S, kt_desc + stage + 128 * kk, terms + 128 * kk, id_s,
+            tc::mma_bf16(tmem + T_S, kt_desc + k_at + 128 * kk, terms + 128 * kk, id_s,
                          !STATES || c > 0 || kk > 0);
           if (STATES) {
             tc::commit(&B.vt_empty[s]);
-            tc::commit(&B.empty[s]);
+            tc::commit(&B.k_empty[s]);
             continue;
           }
           tc::commit(&B.s_full);
+          tc::commit(&B.k_empty[s]);  // Q Kᵀ is done too
           // the masked products times V
           ok = wait_bar(&B.pt_full, c, D.err) &&
                (c == 0 || wait_bar(&B.o_empty[s ^ 1], (c - 1) >> 1, D.err));
@@ -500,9 +527,9 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
 #pragma unroll 2
           for (int kk = 0; kk < CH / 16; ++kk)
             tc::mma_bf16_a_tmem(tmem + T_O, tmem + T_P + 32 * (kk >> 1) + 8 * (kk & 1),
-                                v_desc + stage + 128 * kk, id_o, kk > 0);
+                                v_desc + v_at + 128 * kk, id_o, kk > 0);
           tc::commit(&B.o_full);
-          tc::commit(&B.empty[s]);
+          tc::commit(&B.v_empty[s]);
         }
         if (c + 1 < n) {
           scores(c + 1);
@@ -622,6 +649,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     const int tid = threadIdx.x - 32 * 16;
     const uint32_t sign = D.scale < 0.f ? 0x80008000u : 0u;
     float e = 0.f;
+    int vs = 0, vp = 0;  // v's slot and phase
 #pragma unroll 1
     for (int c = 0; c <= n; ++c) {
       const float e_prev = e;
@@ -632,13 +660,14 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
           if (tid == 64) B.anybad[c & 3] = 0;
           named_bar_sync(1, 256);
         }
-        if (!wait(&B.full[s], c >> 1) || !wait(&B.gate_full[s], c >> 1)) break;
+        if (!wait(&B.v_full[vs], vp) || !wait(&B.gate_full[s], c >> 1)) break;
         const float w = B.gate[s].w[j];
         if (!STATES) e = B.gate[s].e[j];
-        unsigned char* st = base + s * STAGE;
-        unsigned char* v = st + QB + 128 * j;
+        unsigned char* v = vb + vs * VB + 128 * j;
         unsigned char* to = vt + 3 * VB * (c & (NV - 1)) + 128 * j;
         const int sw = j & 7;
+        // the rows of k behind a sequence are cleared below
+        if (t - lane + 32 > it.t1 && !wait(&B.k_full[s], c >> 1)) break;
         if (!(STATES ? wait(&B.vt_empty[s], (c >> 1) + 1) : c == 0 || wait(&B.s_full, c - 1)))
           break;
         uint32_t odd = 0;  // NaN (in either half) once a value of v is infinite or NaN
@@ -653,7 +682,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
             *reinterpret_cast<uint4*>(v + at) = word;
 #pragma unroll
             for (int x = 0; x < DK / 64; ++x)
-              *reinterpret_cast<uint4*>(st + 16384 * x + 128 * j + at) = word;
+              *reinterpret_cast<uint4*>(base + s * QB + 16384 * x + 128 * j + at) = word;
           }
           const uint32_t in[4] = {word.x, word.y, word.z, word.w};
           uint32_t hi[4], mid[4], lo[4];
@@ -674,7 +703,11 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         if (odd & 0x7FFF7FFFu) mark_row(v, to, sw, half, j, B.colbad[c & 3], &B.anybad[c & 3]);
         tc::fence_async_smem();
         arrive(&B.vt_full);
-        if (lane == 0) mbar_arrive(&B.gate_empty[s]);
+        if (lane == 0) {
+          mbar_arrive(&B.gate_empty[s]);
+          if (STATES) mbar_arrive(&B.v_empty[vs]);
+        }
+        if (++vs == RV) vs = 0, vp ^= 1;
       }
       if (!STATES && c > 0) {
         const int cc = c - 1, t = it.t0 + CH * cc + j;
@@ -744,7 +777,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
     const bool mine = 32 * quad < DK;
     float* row = D.state + (((size_t)it.row * D.HV + h) * DK + d) * D.DV + c0;
-    const float* left = W0 + (size_t)d * D.DV + c0;  // what segment 0 leaves behind
+    float* left = W0 + (size_t)d * D.DV + c0;  // what segment 0 leaves behind
     // 16 columns at a time; `x` of the functions below is their first column
     float S[16];
     auto load = [&](const float* from, float f) {
@@ -803,7 +836,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
             from_tmem(x);
           } else if (it.seg == 0) {
             clear();
-            load(row + x, 1.f);
+            load((it.nseg == 1 ? row : left + (size_t)(it.nseg - 1) * D.HV * plane) + x, 1.f);
           } else {
             join(x, it.seg);
           }
@@ -835,13 +868,9 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         if (STATES) {
           from_tmem(x);
           if (it.seg == 0) load(row + x, ex2((float)B.g_total));
-          store(const_cast<float*>(left) + (size_t)it.seg * D.HV * plane + x);
-        } else if (it.nseg == 1) {
+          store(left + (size_t)it.seg * D.HV * plane + x);
+        } else if (it.seg == it.nseg - 1) {
           from_tmem(x);
-          store(row + x);
-        } else if (it.seg == 0) {
-          // the only segment that reads the state's row writes it
-          join(x, it.nseg);
           store(row + x);
         }
       }
@@ -861,12 +890,11 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   }
 }
 
-// k, v twice; three terms of Ṽ, q, S and o (twice the terms for STATES); the rest,
-// alignment.
+// k twice; v twice, three terms of Ṽ, q, S and o (STATES: v three times, the terms twice);
+// the rest, alignment.
 constexpr int chunk_smem(int DK) {
-  constexpr int terms = 3 * 16384;
-  const int main = terms + 256 * DK + 128 * DK + 16384;
-  return 2 * (256 * DK + 16384) + (main > 2 * terms ? main : 2 * terms) + 10240;
+  const int walk = 5 * 16384 + 256 * DK + 128 * DK + 16384, states = 9 * 16384;
+  return 512 * DK + (walk > states ? walk : states) + 10240;
 }
 
 // Tokens of a segment: so many that the segments of one sequence of T tokens give
