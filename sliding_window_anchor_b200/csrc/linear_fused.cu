@@ -67,41 +67,6 @@ __device__ __forceinline__ void store_one(const FusedParams& P, int t, int f, fl
     static_cast<uint16_t*>(P.y)[t * P.ldy + f] = f2bf(v);
 }
 
-// Adds the residual to four values of token t, features f.., and stores them.
-__device__ __forceinline__ void finish_four(const FusedParams& P, int t, int f,
-                                            const float (&v)[4]) {
-  const bool all = f + 4 <= P.F;
-  const int64_t to = t * P.ldy + f, from = t * P.ldr + f;
-  if (P.f32) {
-    float* y = static_cast<float*>(P.y) + to;
-    const float* r = static_cast<const float*>(P.residual) + from;
-    if (all && ((uintptr_t)y & 15u) == 0 && (!P.residual || ((uintptr_t)r & 15u) == 0)) {
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (P.residual) a = *reinterpret_cast<const float4*>(r);
-      *reinterpret_cast<float4*>(y) =
-          make_float4(v[0] + a.x, v[1] + a.y, v[2] + a.z, v[3] + a.w);
-      return;
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (f + j < P.F) y[j] = v[j] + (P.residual ? r[j] : 0.f);
-  } else {
-    uint16_t* y = static_cast<uint16_t*>(P.y) + to;
-    const uint16_t* r = static_cast<const uint16_t*>(P.residual) + from;
-    if (all && ((uintptr_t)y & 7u) == 0 && (!P.residual || ((uintptr_t)r & 7u) == 0)) {
-      uint2 a = make_uint2(0u, 0u);
-      if (P.residual) a = *reinterpret_cast<const uint2*>(r);
-      *reinterpret_cast<uint2*>(y) =
-          make_uint2(pack2_bf(v[0] + bf_lo(a.x), v[1] + bf_hi(a.x)),
-                     pack2_bf(v[2] + bf_lo(a.y), v[3] + bf_hi(a.y)));
-      return;
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (f + j < P.F) y[j] = f2bf(v[j] + (P.residual ? bf1(r[j]) : 0.f));
-  }
-}
-
 // Bias of features f..f+31 (the same for every lane).
 __device__ __forceinline__ void add_bias32(float (&v)[32], const FusedParams& P, int f) {
   if (!P.bias) return;
@@ -334,9 +299,17 @@ struct DenseParams {
   int n_m, n_n, KB, S;
   int x_rows;               // token rows a CTA fetches: 128, fewer when T has fewer
   int tma_y;
-  int vec_r;                // residual rows in 16-byte loads
+  int vec_r, vec_y;         // residual and y rows are whole 16-byte units
   int32_t* err;
 };
+
+__device__ __forceinline__ float4 lds_f4(uint32_t a) {
+  float4 r;
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w)
+               : "r"(a));
+  return r;
+}
 
 // Tile order: eight token tiles side by side, then along the features, so that
 // the pairs at work share weight rows and token rows in L2.
@@ -572,88 +545,133 @@ __global__ void __launch_bounds__(DN_THREADS, 1) k_dense(const __grid_constant__
       }
       if (lane == 0) tc::bulk_wait_all();
     } else {
-      // this share's sums: [128 tokens][BN], 16-byte chunk c of row t at c ^ t % 8
-      const bool ok = mbar_wait(&B.tfull[0], 0, P.err);
-      if (!ok) B.failed = 1;
-      tc::fence_after_sync();
-      const int row = 32 * quad + lane;
-      if (__all_sync(0xffffffffu, ok)) {
-        float* sums = reinterpret_cast<float*>(base);
-#pragma unroll 1
-        for (int cb = 0; cb < BN / 64; ++cb) {
-          const int col = BN / 2 * half + 32 * cb;
-          uint32_t r[32];
-          tc::tmem_ld32(tmem + lanes + col, r);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<uint4*>(sums + BN * row + 4 * ((col / 4 + i) ^ (row & 7))) =
-                make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
-        }
-      }
-      tc::fence_before_sync();
+      if (!__all_sync(0xffffffffu, mbar_wait(&B.tfull[0], 0, P.err))) B.failed = 1;
     }
   }
   if (P.S > 1) {
-    // share p finishes rows [rows p / S, rows (p + 1) / S) of its CTA's tokens: every
-    // other share's sums of these rows come here in one bulk copy each
-    tc::fence_async_smem();
+    // Share p finishes rows [rows p / S, rows (p + 1) / S) of its CTA's tokens.  A warp of
+    // the epilogue writes its sums (32 tokens, half of the columns; [half][token][BN/2],
+    // 16-byte chunk c of row t at c ^ t % 8) and copies the rows that other shares finish
+    // to these, one bulk copy each.
     tc::cluster_sync();  // every CTA of the cluster is past its products
     int m, n;
     tile_at(P, cluster, m, n);
     const int t0 = 256 * m + 128 * rank;
     const int rows = max(0, min(128, P.f.T - t0));
     const int r0 = rows * share / P.S, r1 = rows * (share + 1) / P.S;
-    const int slot = (rows + P.S - 1) / P.S * BN;  // floats of one share's rows
-    const float* sums = reinterpret_cast<const float*>(base);
-    const float* others = sums + 128 * BN;
-    if (threadIdx.x == 0) {
+    const int slot = (rows + P.S - 1) / P.S;  // rows kept for another share's sums
+    constexpr int HB = BN / 2;
+    float* sums = reinterpret_cast<float*>(base);
+    float* others = sums + 128 * BN;  // [share][half][slot][HB]
+    if (threadIdx.x == 0)
       mbar_arrive_expect_tx(&B.got, (uint32_t)((P.S - 1) * (r1 - r0) * BN * 4));
-      for (int p = 0; p < P.S; ++p) {
-        const int q0 = rows * p / P.S, q1 = rows * (p + 1) / P.S;
-        if (p == share || q0 == q1) continue;
-        const uint32_t to = tc::map_to_rank(others + (size_t)slot * (share - (share > p)),
-                                            2 * p + rank);
-        tc::bulk_s2peer(to, sums + (size_t)BN * q0, (uint32_t)((q1 - q0) * BN * 4),
-                        tc::map_to_rank(&B.got, 2 * p + rank));
+    if (warp < 8 && !B.failed) {
+      const int quad = warp & 3, half = warp >> 2, row = 32 * quad + lane;
+      float* mine = sums + half * 128 * HB;
+      tc::fence_after_sync();
+#pragma unroll 1
+      for (int col = 0; col < HB; col += 32) {
+        uint32_t r[32];
+        tc::tmem_ld32(tmem + ((uint32_t)(32 * quad) << 16) + HB * half + col, r);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4*>(mine + HB * row + 4 * ((col / 4 + i) ^ (row & 7))) =
+              make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+      }
+      tc::fence_before_sync();
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane < P.S && lane != share) {
+        const int p = lane;
+        const int q0 = max(rows * p / P.S, 32 * quad);
+        const int q1 = min(rows * (p + 1) / P.S, 32 * quad + 32);
+        if (q0 < q1) {
+          float* at = others + ((size_t)(2 * (share - (share > p)) + half) * slot +
+                                (q0 - rows * p / P.S)) * HB;
+          tc::bulk_s2peer(tc::map_to_rank(at, 2 * p + rank), mine + HB * q0,
+                          (uint32_t)((q1 - q0) * HB * 4),
+                          tc::map_to_rank(&B.got, 2 * p + rank));
+        }
       }
     }
+    named_bar_sync(1, DN_THREADS);  // this CTA's own sums are in place
     if (threadIdx.x < DN_EPI && !mbar_wait(&B.got, 0, P.err)) B.failed = 1;
     if (threadIdx.x < DN_EPI && !B.failed) {
-      // a thread keeps its four features and walks down the rows
+      // a thread keeps its four features and walks down the rows; a row's loads are issued
+      // together (four shares' always, their sums by need: a branch between them made
+      // each wait for the one before)
       constexpr int GR = FT / 4;
       static_assert(DN_EPI % GR == 0, "");
       const int c = threadIdx.x % GR, f = FT * n + 4 * c;
+      const int c_in = c % (HB / 4), half = c / (HB / 4);  // gated: half 0, up in half 1
       float bias[4] = {};
       if (P.f.bias)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           if (f + j < P.f.F) bias[j] = bf1(P.f.bias[f + j]);
-      const float* from[4];
-#pragma unroll
-      for (int p = 0; p < 4; ++p)
-        from[p] = p == share || p >= P.S ? sums + BN * r0
-                                         : others + (size_t)slot * (p - (p > share));
       const int S = P.S;
-      if (f < P.f.F) {
-#pragma unroll 2
-        for (int r = threadIdx.x / GR; r < r1 - r0; r += DN_EPI / GR) {
-          const int x = (r0 + r) & 7;
-          const int at = BN * r + 4 * (c ^ x), at_u = BN * r + 4 * ((GR + c) ^ x);
-          float v[4] = {bias[0], bias[1], bias[2], bias[3]}, u[4] = {};
+      uint32_t from[4], second[4];  // shared-memory addresses; the gated product's up sums
 #pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            if (p >= S) break;
-            const float4 a = *reinterpret_cast<const float4*>(from[p] + at);
-            v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
-            if (GATED) {
-              const float4 b = *reinterpret_cast<const float4*>(from[p] + at_u);
-              u[0] += b.x, u[1] += b.y, u[2] += b.z, u[3] += b.w;
-            }
+      for (int p = 0; p < 4; ++p) {
+        const bool own = p == share || p >= S;
+        const float* at = own ? sums + (half * 128 + r0) * HB
+                              : others + (size_t)(2 * (p - (p > share)) + half) * slot * HB;
+        from[p] = smem_u32(at);
+        second[p] = from[p] + 4 * HB * (own ? 128 : slot);
+      }
+      const int el = P.f.f32 ? 4 : 2;
+      const bool vec = f + 4 <= P.f.F && P.vec_y && (!P.f.residual || P.vec_r);
+      char* y = static_cast<char*>(P.f.y) + ((int64_t)(t0 + r0) * P.f.ldy + f) * el;
+      const char* res = static_cast<const char*>(P.f.residual) +
+                        ((int64_t)(t0 + r0) * P.f.ldr + f) * el;
+#pragma unroll 1
+      for (int r = threadIdx.x / GR; r < r1 - r0 && f < P.f.F; r += DN_EPI / GR) {
+        const uint32_t at = 4 * (HB * r + 4 * (c_in ^ ((r0 + r) & 7)));
+        float4 a[4], b[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          a[p] = lds_f4(from[p] + at);
+          if (GATED) b[p] = lds_f4(second[p] + at);
+        }
+        float4 v = make_float4(bias[0], bias[1], bias[2], bias[3]);
+        float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+          if (p < S) {
+            v.x += a[p].x, v.y += a[p].y, v.z += a[p].z, v.w += a[p].w;
+            if (GATED) u.x += b[p].x, u.y += b[p].y, u.z += b[p].z, u.w += b[p].w;
           }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = activate(v[j], ACT) * (GATED ? u[j] : 1.f);
-          finish_four(P.f, t0 + r0 + r, f, v);
+        v.x = activate(v.x, ACT), v.y = activate(v.y, ACT);
+        v.z = activate(v.z, ACT), v.w = activate(v.w, ACT);
+        if (GATED) v.x *= u.x, v.y *= u.y, v.z *= u.z, v.w *= u.w;
+        char* to = y + (int64_t)r * P.f.ldy * el;
+        const char* add = res + (int64_t)r * P.f.ldr * el;
+        if (vec && el == 4) {
+          if (P.f.residual) {
+            const float4 b = *reinterpret_cast<const float4*>(add);
+            v.x += b.x, v.y += b.y, v.z += b.z, v.w += b.w;
+          }
+          *reinterpret_cast<float4*>(to) = v;
+        } else if (vec) {
+          if (P.f.residual) {
+            const uint2 b = *reinterpret_cast<const uint2*>(add);
+            v.x += bf_lo(b.x), v.y += bf_hi(b.x), v.z += bf_lo(b.y), v.w += bf_hi(b.y);
+          }
+          *reinterpret_cast<uint2*>(to) = make_uint2(pack2_bf(v.x, v.y), pack2_bf(v.z, v.w));
+        } else {
+#pragma unroll 1
+          for (int j = 0; j < 4 && f + j < P.f.F; ++j) {
+            float x = v.x;
+            v.x = v.y, v.y = v.z, v.z = v.w;
+            if (P.f.residual)
+              x += el == 4 ? reinterpret_cast<const float*>(add)[j]
+                           : bf1(reinterpret_cast<const uint16_t*>(add)[j]);
+            if (el == 4)
+              reinterpret_cast<float*>(to)[j] = x;
+            else
+              reinterpret_cast<uint16_t*>(to)[j] = f2bf(x);
+          }
         }
       }
     }
@@ -786,6 +804,7 @@ int launch_dense(const FusedParams& F, int32_t* err, cudaStream_t st) {
   // a TMA store rounds a clipped row up to 16 bytes
   P.tma_y = plan.S == 1 && aligned16(F.y) && F.ldy * el % 16 == 0 && F.F * el % 16 == 0;
   P.vec_r = aligned16(F.residual) && F.ldr * el % 16 == 0;
+  P.vec_y = aligned16(F.y) && F.ldy * el % 16 == 0;
   P.x_rows = F.T >= 128 ? 128 : (F.T + 7) / 8 * 8;
   if (!encode_rows(&P.x_map, F.x, false, F.K, F.T, F.ldx * 2, 64, P.x_rows) ||
       !encode_rows(&P.w_map, F.w, false, F.K, F.F, (uint64_t)F.K * 2, 64, plan.BN / 2) ||
