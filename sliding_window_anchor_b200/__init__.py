@@ -379,6 +379,14 @@ def gated_linear(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act=
     return out
 
 
+def _index(t, device, name):
+    """A list or tensor of int32 on the call's device."""
+    t = _ids(t, device)
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return t
+
+
 def _decay_shape(state, q, v):
     if state.dim() != 4 or q.dim() != 3 or v.dim() != 3:
         raise ValueError("state must be [rows, v_heads, k_dim, v_dim], q, k [T, k_heads, k_dim], "
@@ -413,7 +421,7 @@ def decay_decode(state: torch.Tensor, seq_ids, q, k, v, log_decay, scale=None, o
     v_dim] (rows may be strided: slices of one projection), log_decay FP32 [B, v_heads] or
     [v_heads]; scale defaults to k_dim ** -0.5; returns o BF16 [B, v_heads, v_dim]."""
     device = _device_of(state, "state")
-    ids = _ids(seq_ids, device)
+    ids = _index(seq_ids, device, "seq_ids")
     B = ids.numel()
     sh = _decay_shape(state, q, v)
     rows, out = _decay_rows(device, sh, B, q, k, v, log_decay, scale, out)
@@ -437,13 +445,15 @@ def decay_prefill(state: torch.Tensor, seq_ids, cu_tokens, q, k, v, log_decay, s
     of T packed rows of q, k, v, log_decay and out; the rest as in decay_decode, which it
     equals token by token."""
     device = _device_of(state, "state")
-    ids, cu = _ids(seq_ids, device), _ids(cu_tokens, device)
+    ids, cu = _index(seq_ids, device, "seq_ids"), _index(cu_tokens, device, "cu_tokens")
     B, T = ids.numel(), q.shape[0]
     if cu.numel() != B + 1:
         raise ValueError(f"cu_tokens must have {B + 1} entries, got {cu.numel()}")
     sh = _decay_shape(state, q, v)
     rows, out = _decay_rows(device, sh, T, q, k, v, log_decay, scale, out)
     nb = int(lib().er_decay_prefill_workspace_bytes(sh, B, T)) if B else 0
+    if ws is not None and ws.device != device:
+        raise ValueError(f"ws must be on {device}, got {ws.device}")
     ws = _ws(nb, device, ws)
     _call("er_decay_prefill", device,
           _dense(state, device, torch.float32, state.shape, "state"), state.shape[0],

@@ -197,6 +197,46 @@ def test_nan_stays_in_its_head_and_behind_its_token(sab):
     assert torch.equal(N[a, heads], S[a, heads])
 
 
+@pytest.mark.parametrize("n,at", [(1, 0), (150, 0), (150, 63), (150, 149), (300, 130), (2000, 700)])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_non_finite_values_reach_no_earlier_token(sab, n, at, bad):
+    """An infinite or NaN v: its column of its head from its token on, and of the state; k:
+    its head from its token on; q: its own token's heads.  Nothing in front, beside, or of
+    another sequence."""
+    c = Case([n, 90], 2, 4, 128, 64, rate=(-5, -3))
+    S = c.state.clone()
+    clean = sab.decay_prefill(S, c.ids, c.cu, c.q, c.k, c.v, c.g)
+    a, b = c.ids.tolist()
+
+    def spoiled(part, where):
+        keep = part[at][where].clone()
+        part[at][where] = bad
+        N = c.state.clone()
+        o = sab.decay_prefill(N, c.ids, c.cu, c.q, c.k, c.v, c.g)
+        part[at][where] = keep
+        assert torch.equal(o[:at], clean[:at]) and torch.equal(o[n:], clean[n:])
+        assert torch.equal(N[b], S[b])
+        return o, N
+
+    o, N = spoiled(c.v, (1, 37))
+    rest = torch.ones(4, 64, dtype=torch.bool, device="cuda")
+    rest[1, 37] = False
+    assert torch.equal(o[:, rest], clean[:, rest])
+    assert not bool(o[at:n, 1, 37].isfinite().any())
+    assert torch.equal(N[a].transpose(1, 2)[rest], S[a].transpose(1, 2)[rest])
+    assert not bool(N[a, 1, :, 37].isfinite().any())
+
+    o, N = spoiled(c.k, (0, 5))  # heads 0 and 1
+    assert torch.equal(o[:, 2:], clean[:, 2:]) and torch.equal(N[a, 2:], S[a, 2:])
+    assert not bool(o[at, :2].isfinite().any())
+    assert not bool(N[a, :2, 5].isfinite().any())
+
+    o, N = spoiled(c.q, (1, 0))  # heads 2 and 3
+    assert torch.equal(N, S) and torch.equal(o[:, :2], clean[:, :2])
+    assert torch.equal(o[at + 1:], clean[at + 1:])
+    assert not bool(o[at, 2:].isfinite().any())
+
+
 def test_bad_rows_are_skipped_and_told(sab):
     """State rows out of range or listed twice, rows of tokens out of range."""
     c = Case([60, 70, 80, 90], 2, 2, 64, 64, rows=6)
@@ -233,7 +273,7 @@ def test_bad_rows_are_skipped_and_told(sab):
             assert fine or torch.equal(S[row], c.state[row])
 
 
-@pytest.mark.parametrize("lengths", [[1] * 5, [300, 20]])
+@pytest.mark.parametrize("lengths", [[1] * 5, [300, 20], [3000, 7]])
 def test_captured_calls_and_streams(sab, lengths):
     c = Case(lengths, 2, 4, 128, 128)
     decode = max(lengths) == 1
@@ -318,6 +358,9 @@ def test_refusals_on_the_gpu(sab):
         S = torch.zeros(2, 4, 32, 64, device="cuda")
         qk = c.q[:2, :, :32].contiguous()
         sab.decay_decode(S, [0, 1], qk, qk, c.v[:2], c.g[:2])
+    with pytest.raises(ValueError):
+        sab.decay_decode(c.state, torch.zeros(2, dtype=torch.int32), *(x[:2] for x in a),
+                         dev_error=torch.zeros(1, dtype=torch.int32))
     n = sab.launch_count()
     empty = torch.empty(0, dtype=torch.int32, device="cuda")
     assert sab.decay_decode(c.state, empty, *(x[:0] for x in a)).shape == (0, 4, 64)

@@ -153,6 +153,20 @@ def test_row_strides_and_what_lies_between(sab, T, fp32, ldy):
             assert bool((flat[:shift] == 7).all())
 
 
+@pytest.mark.parametrize("T", [3, 40, 300])
+@pytest.mark.parametrize("F", [256, 1001])
+def test_bias_from_an_odd_element(sab, T, F):
+    """Bias and weights that start inside a larger tensor (the bias off 16 bytes)."""
+    K = 136
+    x, w = normal(1, T, K), normal(2, F + 3, K, scale=K ** -0.5)[3:]
+    b = normal(3, F + 5)[5:]
+    for fp32 in (False, True):
+        close(sab.linear_fused(x, w, bias=b, fp32_out=fp32),
+              linear64(x, w, b, "none", None, fp32))
+    g = normal(4, 2 * F, K, scale=K ** -0.5)  # the halves of one stacked weight
+    close(sab.gated_linear(x, g[:F], g[F:]), gated64(x, g[:F], g[F:], "silu", False))
+
+
 @pytest.mark.parametrize("T", [1, 24, 90, 520])
 def test_residual_in_place_and_repeats(sab, T):
     """The residual may be the output; the same inputs give the same bits."""
