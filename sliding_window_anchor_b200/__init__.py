@@ -431,6 +431,7 @@ def decay_decode(state: torch.Tensor, seq_ids, q, k, v, log_decay, scale=None, o
     return out
 
 
+@functools.lru_cache(maxsize=256)
 def decay_prefill_workspace_bytes(k_heads: int, v_heads: int, k_dim: int, v_dim: int, B: int,
                                   T: int) -> int:
     return int(lib().er_decay_prefill_workspace_bytes(
@@ -451,7 +452,7 @@ def decay_prefill(state: torch.Tensor, seq_ids, cu_tokens, q, k, v, log_decay, s
         raise ValueError(f"cu_tokens must have {B + 1} entries, got {cu.numel()}")
     sh = _decay_shape(state, q, v)
     rows, out = _decay_rows(device, sh, T, q, k, v, log_decay, scale, out)
-    nb = int(lib().er_decay_prefill_workspace_bytes(sh, B, T)) if B else 0
+    nb = decay_prefill_workspace_bytes(sh.k_heads, sh.v_heads, sh.k_dim, sh.v_dim, B, T) if B else 0
     if ws is not None and ws.device != device:
         raise ValueError(f"ws must be on {device}, got {ws.device}")
     ws = _ws(nb, device, ws)

@@ -160,8 +160,8 @@ int launch_decode(const DecayParams& P, cudaStream_t st) {
 //
 // A CTA walks 64 columns of one value head through one segment of a sequence.
 // Long sequences are cut into segments of L tokens that are walked at the same time:
-// a first launch (STATES) finds what each segment's own tokens leave behind, and a
-// segment's walk starts from those of the segments in front of it.  There a
+// a first launch (STATES) finds what each segment's own tokens leave behind, a second one
+// what the segments in front of each leave together, which its walk starts from.  There a
 // segment's chunks are walked from its end, so that all decays are known and no
 // product waits for another.
 //
@@ -200,7 +200,9 @@ struct Item {
   int found, row, b, seg, nseg, slot, t0, t1;
 };
 
-// Segment `index` of the call's sequences, by one warp; reports bad rows.
+// Segment `index` of the call's sequences, or the first one of sequence `index`, by one
+// warp; reports bad rows.
+template <bool SEQUENCE>
 __device__ __forceinline__ void find_item(const DecayParams& P, int L, int index, Item* out) {
   const int lane = threadIdx.x & 31;
   int acc = 0, slots = 0;
@@ -236,12 +238,21 @@ __device__ __forceinline__ void find_item(const DecayParams& P, int L, int index
       const int x = __shfl_up_sync(0xffffffffu, sum, m), y = __shfl_up_sync(0xffffffffu, many, m);
       if (lane >= m) sum += x, many += y;
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, acc + sum > index);
+    const unsigned hit =
+        __ballot_sync(0xffffffffu, SEQUENCE ? b == index && n > 0 : acc + sum > index);
     if (hit) {
       const int l = __ffs(hit) - 1;
+      // an earlier sequence with the same state row?
+      const int same_as = __shfl_sync(0xffffffffu, row, l);
+      bool same = lane < l && row == same_as;
+      for (int j = lane; j < b0; j += 32) same |= P.seq_ids[j] == same_as;
+      if (__any_sync(0xffffffffu, same)) {
+        if (lane == 0) set_dev_error(P.err, ER_EINVAL), *out = it;
+        return;
+      }
       if (lane == l) {
         it.found = 1, it.row = row, it.b = b, it.nseg = n;
-        it.seg = index - (acc + sum - n);
+        it.seg = SEQUENCE ? 0 : index - (acc + sum - n);
         it.slot = slots + many - (n > 1 ? n : 0);
         it.t0 = begin + L * it.seg;
         it.t1 = min(end, it.t0 + L);
@@ -349,9 +360,15 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   const int h = blockIdx.x % per / slices, c0 = 64 * (blockIdx.x % slices);
   const int hk = h / (D.HV / D.HK);
 
+  if (threadIdx.x == 64) {
+    // launch arguments: no earlier kernel writes them
+    tc::prefetch_map(&P.k_map);
+    tc::prefetch_map(&P.v_map);
+    if (!STATES) tc::prefetch_map(&P.q_map);
+  }
   grid_dep_wait();
   grid_dep_trigger();
-  if (warp == 0) find_item(D, P.L, blockIdx.x / per, &B.item);
+  if (warp == 0) find_item<false>(D, P.L, blockIdx.x / per, &B.item);
   if (threadIdx.x == 32) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&B.k_full[i], 1);
@@ -382,12 +399,6 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   __syncthreads();
   const Item it = B.item;
   if (!it.found || (STATES && it.nseg < 2)) return;
-  int same = 0;
-  for (int j = threadIdx.x; j < it.b; j += DC_THREADS) same |= D.seq_ids[j] == it.row;
-  if (__syncthreads_or(same)) {
-    if (threadIdx.x == 0) set_dev_error(D.err, ER_EINVAL);
-    return;
-  }
   const size_t plane = (size_t)DK * D.DV;
   float* W0 = P.W + ((size_t)it.slot * D.HV + h) * plane;
   if (STATES && it.seg == it.nseg - 1) {
@@ -788,20 +799,6 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         S[i + 2] = fmaf(f, y.z, S[i + 2]), S[i + 3] = fmaf(f, y.w, S[i + 3]);
       }
     };
-    auto clear = [&]() {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) S[i] = 0.f;
-    };
-    // what the first `segs` segments leave behind, together
-    auto join = [&](int x, int segs) {
-      clear();
-      double R = 0.0;
-#pragma unroll 1
-      for (int g = segs - 1; g >= 0; --g) {
-        load(left + (size_t)g * D.HV * plane + x, ex2((float)R));
-        R += P.Wg[(size_t)(it.slot + g) * D.HV + h];
-      }
-    };
     auto from_tmem = [&](int x) {
       uint32_t hi[16], mid[16], lo[16];
       tc::tmem_ld16(tmem + lanes + T_S + x, hi);
@@ -818,6 +815,33 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         *reinterpret_cast<float4*>(to + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
     };
     bool ok = true;
+    if (!STATES && mine) {
+      // the state that the walk starts from, through TMEM like every later one: the row, its
+      // copy in the last segment's slot, or what the segments in front leave together
+      const float* from = it.nseg == 1 ? row : left + (size_t)((it.seg ? it.seg : it.nseg) - 1) *
+                                                          D.HV * plane;
+#pragma unroll 1
+      for (int x = 0; x < 64; x += 32) {
+        float4 y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = *reinterpret_cast<const float4*>(from + x + 4 * i);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t r[16];
+          const uint32_t zero[16] = {};
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            r[4 * m] = __float_as_uint(y[4 * i + m].x), r[4 * m + 1] = __float_as_uint(y[4 * i + m].y);
+            r[4 * m + 2] = __float_as_uint(y[4 * i + m].z);
+            r[4 * m + 3] = __float_as_uint(y[4 * i + m].w);
+          }
+          tc::tmem_st16(tmem + lanes + T_S + x + 16 * i, r);
+          tc::tmem_st16(tmem + lanes + T_S + 64 + x + 16 * i, zero);
+          tc::tmem_st16(tmem + lanes + T_S + 128 + x + 16 * i, zero);
+        }
+      }
+      tc::tmem_wait_st();
+    }
 #pragma unroll 1
     for (int c = 0; !STATES && c < n; ++c) {
       if (c > 0) {
@@ -832,14 +856,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         const uint32_t zero[16] = {};
 #pragma unroll 1
         for (int x = 0; x < 64; x += 16) {
-          if (c > 0) {
-            from_tmem(x);
-          } else if (it.seg == 0) {
-            clear();
-            load((it.nseg == 1 ? row : left + (size_t)(it.nseg - 1) * D.HV * plane) + x, 1.f);
-          } else {
-            join(x, it.seg);
-          }
+          from_tmem(x);
 #pragma unroll
           for (int i = 0; i < 2; ++i)
             *reinterpret_cast<uint4*>(sb + 128 * d + 16 * ((x / 8 + i) ^ (d & 7))) = make_uint4(
@@ -887,6 +904,44 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   if (warp == DC_MMA) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// What each segment's own tokens leave behind becomes what all segments up to it leave
+// together: W[g] += e^{G_g} W[g - 1], for the segments that a later one starts from.  Four
+// values a thread, eight segments' loads in flight.
+constexpr int DJ_THREADS = 256;
+__global__ void __launch_bounds__(DJ_THREADS) k_decay_join(const ChunkParams P) {
+  __shared__ Item item;
+  const DecayParams& D = P.d;
+  grid_dep_wait();
+  grid_dep_trigger();
+  const int plane = D.DK * D.DV, parts = plane / (4 * DJ_THREADS), per = D.HV * parts;
+  if (threadIdx.x < 32) find_item<true>(D, P.L, blockIdx.x / per, &item);
+  __syncthreads();
+  const Item it = item;
+  if (!it.found || it.nseg < 3) return;
+  const int h = blockIdx.x % per / parts, part = blockIdx.x % parts;
+  const size_t step = (size_t)D.HV * plane;
+  float* W = P.W + it.slot * step + (size_t)h * plane + 4 * (part * DJ_THREADS + threadIdx.x);
+  const double* G = P.Wg + (size_t)it.slot * D.HV + h;
+  float4 s = *reinterpret_cast<const float4*>(W);
+  for (int g0 = 1; g0 < it.nseg - 1; g0 += 8) {
+    float4 y[8];
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (g0 + i < it.nseg - 1) {
+        y[i] = *reinterpret_cast<const float4*>(W + (g0 + i) * step);
+        f[i] = ex2((float)G[(g0 + i) * D.HV]);
+      }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (g0 + i < it.nseg - 1) {
+        s.x = fmaf(f[i], s.x, y[i].x), s.y = fmaf(f[i], s.y, y[i].y);
+        s.z = fmaf(f[i], s.z, y[i].z), s.w = fmaf(f[i], s.w, y[i].w);
+        *reinterpret_cast<float4*>(W + (g0 + i) * step) = s;
+      }
   }
 }
 
@@ -952,19 +1007,31 @@ int launch_prefill(const DecayParams& D, void* ws, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   const size_t segs = (size_t)D.B + (D.T > P.L ? D.T / P.L : 0);
   const size_t blocks = segs * D.HV * (D.DV / 64);
-  if (blocks > 0x7FFFFFFFu) return ER_EINVAL;
+  const size_t parts = (size_t)D.B * D.HV * (D.DK * D.DV / (4 * DJ_THREADS));  // of the second launch
+  if (blocks > 0x7FFFFFFFu || parts > 0x7FFFFFFFu) return ER_EINVAL;
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(DC_THREADS);
   cfg.dynamicSmemBytes = chunk_smem(D.DK);
   cfg.stream = st;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  for (int pass = D.T > P.L ? 0 : 1; pass < 2; ++pass) {
-    const auto fn = D.DK == 64 ? (pass ? k_decay_chunks<64, false> : k_decay_chunks<64, true>)
-                               : (pass ? k_decay_chunks<128, false> : k_decay_chunks<128, true>);
-    if (cudaLaunchKernelEx(&cfg, fn, P) != cudaSuccess) return ER_ECUDA;
+  const bool wide = D.DK == 128;
+  if (D.T > P.L) {
+    if (cudaLaunchKernelEx(&cfg, wide ? k_decay_chunks<128, true> : k_decay_chunks<64, true>, P) !=
+        cudaSuccess)
+      return ER_ECUDA;
+    count_launches(1);
+    cudaLaunchConfig_t join = cfg;
+    join.gridDim = dim3((unsigned)parts);
+    join.blockDim = dim3(DJ_THREADS);
+    join.dynamicSmemBytes = 0;
+    if (cudaLaunchKernelEx(&join, k_decay_join, P) != cudaSuccess) return ER_ECUDA;
     count_launches(1);
   }
+  if (cudaLaunchKernelEx(&cfg, wide ? k_decay_chunks<128, false> : k_decay_chunks<64, false>, P) !=
+      cudaSuccess)
+    return ER_ECUDA;
+  count_launches(1);
   return launch_status();
 }
 
