@@ -67,12 +67,46 @@ __device__ __forceinline__ void store_one(const FusedParams& P, int t, int f, fl
     static_cast<uint16_t*>(P.y)[t * P.ldy + f] = f2bf(v);
 }
 
-// Bias of features f..f+31 (the same for every lane).
-__device__ __forceinline__ void add_bias32(float (&v)[32], const FusedParams& P, int f) {
+// Adds the residual to four values of token t, features f.., and stores them; `vec`: all
+// four are there, in rows of y (and the residual) that are whole 16-byte units.
+__device__ __forceinline__ void finish_four(const FusedParams& P, int el, bool vec, int t, int f,
+                                            float4 v) {
+  char* to = static_cast<char*>(P.y) + (t * P.ldy + f) * el;
+  const char* add = static_cast<const char*>(P.residual) + (t * P.ldr + f) * el;
+  if (vec && el == 4) {
+    if (P.residual) {
+      const float4 b = *reinterpret_cast<const float4*>(add);
+      v.x += b.x, v.y += b.y, v.z += b.z, v.w += b.w;
+    }
+    *reinterpret_cast<float4*>(to) = v;
+  } else if (vec) {
+    if (P.residual) {
+      const uint2 b = *reinterpret_cast<const uint2*>(add);
+      v.x += bf_lo(b.x), v.y += bf_hi(b.x), v.z += bf_lo(b.y), v.w += bf_hi(b.y);
+    }
+    *reinterpret_cast<uint2*>(to) = make_uint2(pack2_bf(v.x, v.y), pack2_bf(v.z, v.w));
+  } else {
+#pragma unroll 1
+    for (int j = 0; j < 4 && f + j < P.F; ++j) {
+      float x = v.x;
+      v.x = v.y, v.y = v.z, v.z = v.w;
+      if (P.residual)
+        x += el == 4 ? reinterpret_cast<const float*>(add)[j]
+                     : bf1(reinterpret_cast<const uint16_t*>(add)[j]);
+      if (el == 4)
+        reinterpret_cast<float*>(to)[j] = x;
+      else
+        reinterpret_cast<uint16_t*>(to)[j] = f2bf(x);
+    }
+  }
+}
+
+// Bias of features f..f+15 (the same for every lane).
+__device__ __forceinline__ void add_bias(float (&v)[16], const FusedParams& P, int f) {
   if (!P.bias) return;
-  if (((uintptr_t)P.bias & 15u) == 0 && f + 32 <= P.F) {
+  if (((uintptr_t)P.bias & 15u) == 0 && f + 16 <= P.F) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       const uint4 b = __ldg(reinterpret_cast<const uint4*>(P.bias + f) + i);
       v[8 * i] += bf_lo(b.x), v[8 * i + 1] += bf_hi(b.x);
       v[8 * i + 2] += bf_lo(b.y), v[8 * i + 3] += bf_hi(b.y);
@@ -81,33 +115,33 @@ __device__ __forceinline__ void add_bias32(float (&v)[32], const FusedParams& P,
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
+    for (int i = 0; i < 16; ++i)
       if (f + i < P.F) v[i] += bf1(P.bias[f + i]);
   }
 }
 
-// Residual of token t, features f..f+31.  Plain loads: it may be y itself.
-__device__ __forceinline__ void add_residual32(float (&v)[32], const FusedParams& P, bool vec,
+// Residual of token t, features f..f+15.  Plain loads: it may be y itself.
+__device__ __forceinline__ void add_residual(float (&v)[16], const FusedParams& P, bool vec,
                                                int t, int f) {
   if (!P.residual) return;
   if (P.f32) {
     const float* r = static_cast<const float*>(P.residual) + t * P.ldr + f;
-    if (vec && f + 32 <= P.F) {
+    if (vec && f + 16 <= P.F) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 4; ++i) {
         const float4 b = reinterpret_cast<const float4*>(r)[i];
         v[4 * i] += b.x, v[4 * i + 1] += b.y, v[4 * i + 2] += b.z, v[4 * i + 3] += b.w;
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
+      for (int i = 0; i < 16; ++i)
         if (f + i < P.F) v[i] += r[i];
     }
   } else {
     const uint16_t* r = static_cast<const uint16_t*>(P.residual) + t * P.ldr + f;
-    if (vec && f + 32 <= P.F) {
+    if (vec && f + 16 <= P.F) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         const uint4 b = reinterpret_cast<const uint4*>(r)[i];
         v[8 * i] += bf_lo(b.x), v[8 * i + 1] += bf_hi(b.x);
         v[8 * i + 2] += bf_lo(b.y), v[8 * i + 3] += bf_hi(b.y);
@@ -116,7 +150,7 @@ __device__ __forceinline__ void add_residual32(float (&v)[32], const FusedParams
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
+      for (int i = 0; i < 16; ++i)
         if (f + i < P.F) v[i] += bf1(r[i]);
     }
   }
@@ -470,7 +504,8 @@ __global__ void __launch_bounds__(DN_THREADS, 1) k_dense(const __grid_constant__
       int it = 0;
       for (int tile = cluster; tile < n_tiles; tile += n_clusters, ++it) {
         const int b = it & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(&B.tfull[b], (it >> 1) & 1, P.err)) || B.failed) {
+        const bool ok = mbar_wait(&B.tfull[b], (it >> 1) & 1, P.err) && !B.failed;
+        if (!__all_sync(0xffffffffu, ok)) {
           B.failed = 1;
           break;
         }
@@ -478,65 +513,66 @@ __global__ void __launch_bounds__(DN_THREADS, 1) k_dense(const __grid_constant__
         int m, n;
         tile_at(P, tile, m, n);
         const int t0 = 256 * m + 128 * rank + 32 * quad, t = t0 + lane;
-        constexpr int NC = FT / 64;  // blocks of 32 columns in this warp's half
+        // Sixteen columns at a time (less code to fetch than for 32, for tiles that are few),
+        // into the warp's staging rows of 128 bytes (16-byte chunk c of row l at c ^ l % 8),
+        // from where whole rows go out: FP32 after 32 columns, BF16 after 64.
+        const bool f32 = P.f.f32;
+        const int group = f32 ? 2 : 4;
+        constexpr int NC = FT / 32;  // in this warp's half of the tile's features
 #pragma unroll 1
         for (int cb = 0; cb < NC; ++cb) {
-          const int col = FT / 2 * half + 32 * cb, f = FT * n + col;
-          uint32_t r[32], u[GATED ? 32 : 1];
-          tc::tmem_ld32(tmem + lanes + BN * b + col, r);
-          if constexpr (GATED) tc::tmem_ld32(tmem + lanes + BN * b + FT + col, u);
+          const int col = FT / 2 * half + 16 * cb, f = FT * n + col;
+          uint32_t r[16], u[GATED ? 16 : 1];
+          tc::tmem_ld16(tmem + lanes + BN * b + col, r);
+          if constexpr (GATED) tc::tmem_ld16(tmem + lanes + BN * b + FT + col, u);
           tc::tmem_wait_ld();
           if (t0 >= P.f.T || f >= P.f.F) continue;  // no row, no column of y
-          float v[32];
+          float v[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+          for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
           if constexpr (GATED) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = activate(v[i], ACT) * __uint_as_float(u[i]);
+            for (int i = 0; i < 16; ++i) v[i] = activate(v[i], ACT) * __uint_as_float(u[i]);
           } else {
-            add_bias32(v, P.f, f);
+            add_bias(v, P.f, f);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = activate(v[i], ACT);
-            if (t < P.f.T) add_residual32(v, P.f, P.vec_r, t, f);
+            for (int i = 0; i < 16; ++i) v[i] = activate(v[i], ACT);
+            if (t < P.f.T) add_residual(v, P.f, P.vec_r, t, f);
           }
-          // the block into the warp's staging rows of 128 bytes (chunk c of row l
-          // at c ^ l % 8), whole rows out: FP32 per block, BF16 per two blocks
-          const bool f32 = P.f.f32;
-          const bool first = f32 || (cb & 1) == 0;
-          if (first) {
+          const int part = cb % group;
+          if (part == 0) {
             if (lane == 0) tc::bulk_wait_read<0>();
             __syncwarp();
           }
           if (f32) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<float4*>(stg + 128 * lane + 16 * (i ^ (lane & 7))) =
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<float4*>(stg + 128 * lane + 16 * ((4 * part + i) ^ (lane & 7))) =
                   make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2; ++i) {
               uint4 o;
               o.x = pack2_bf(v[8 * i], v[8 * i + 1]);
               o.y = pack2_bf(v[8 * i + 2], v[8 * i + 3]);
               o.z = pack2_bf(v[8 * i + 4], v[8 * i + 5]);
               o.w = pack2_bf(v[8 * i + 6], v[8 * i + 7]);
               *reinterpret_cast<uint4*>(stg + 128 * lane +
-                                        16 * ((4 * (cb & 1) + i) ^ (lane & 7))) = o;
+                                        16 * ((2 * part + i) ^ (lane & 7))) = o;
             }
           }
-          const bool last = f32 || (cb & 1) || f + 32 >= P.f.F;
-          if (!last) continue;
+          if (part + 1 < group && f + 16 < P.f.F) continue;
+          const int f_first = f - 16 * part;
           if (P.tma_y) {
             tc::fence_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tc::tma_store_2d(&P.y_map, f32 ? f : f - 32 * (cb & 1), t0, stg);
+              tc::tma_store_2d(&P.y_map, f_first, t0, stg);
               tc::bulk_commit();
             }
           } else {
             __syncwarp();
-            copy_rows(P.f, stg, t0, f32 ? f : f - 32 * (cb & 1), f32 ? 32 : 32 + 32 * (cb & 1),
-                      lane);
+            copy_rows(P.f, stg, t0, f_first, 16 * (part + 1), lane);
           }
         }
         tc::fence_before_sync();
@@ -622,9 +658,6 @@ __global__ void __launch_bounds__(DN_THREADS, 1) k_dense(const __grid_constant__
       }
       const int el = P.f.f32 ? 4 : 2;
       const bool vec = f + 4 <= P.f.F && P.vec_y && (!P.f.residual || P.vec_r);
-      char* y = static_cast<char*>(P.f.y) + ((int64_t)(t0 + r0) * P.f.ldy + f) * el;
-      const char* res = static_cast<const char*>(P.f.residual) +
-                        ((int64_t)(t0 + r0) * P.f.ldr + f) * el;
 #pragma unroll 1
       for (int r = threadIdx.x / GR; r < r1 - r0 && f < P.f.F; r += DN_EPI / GR) {
         const uint32_t at = 4 * (HB * r + 4 * (c_in ^ ((r0 + r) & 7)));
@@ -645,34 +678,7 @@ __global__ void __launch_bounds__(DN_THREADS, 1) k_dense(const __grid_constant__
         v.x = activate(v.x, ACT), v.y = activate(v.y, ACT);
         v.z = activate(v.z, ACT), v.w = activate(v.w, ACT);
         if (GATED) v.x *= u.x, v.y *= u.y, v.z *= u.z, v.w *= u.w;
-        char* to = y + (int64_t)r * P.f.ldy * el;
-        const char* add = res + (int64_t)r * P.f.ldr * el;
-        if (vec && el == 4) {
-          if (P.f.residual) {
-            const float4 b = *reinterpret_cast<const float4*>(add);
-            v.x += b.x, v.y += b.y, v.z += b.z, v.w += b.w;
-          }
-          *reinterpret_cast<float4*>(to) = v;
-        } else if (vec) {
-          if (P.f.residual) {
-            const uint2 b = *reinterpret_cast<const uint2*>(add);
-            v.x += bf_lo(b.x), v.y += bf_hi(b.x), v.z += bf_lo(b.y), v.w += bf_hi(b.y);
-          }
-          *reinterpret_cast<uint2*>(to) = make_uint2(pack2_bf(v.x, v.y), pack2_bf(v.z, v.w));
-        } else {
-#pragma unroll 1
-          for (int j = 0; j < 4 && f + j < P.f.F; ++j) {
-            float x = v.x;
-            v.x = v.y, v.y = v.z, v.z = v.w;
-            if (P.f.residual)
-              x += el == 4 ? reinterpret_cast<const float*>(add)[j]
-                           : bf1(reinterpret_cast<const uint16_t*>(add)[j]);
-            if (el == 4)
-              reinterpret_cast<float*>(to)[j] = x;
-            else
-              reinterpret_cast<uint16_t*>(to)[j] = f2bf(x);
-          }
-        }
+        finish_four(P.f, el, vec, t0 + r0 + r, f, v);
       }
     }
   }
@@ -690,6 +696,193 @@ __global__ void __launch_bounds__(DN_THREADS, 1) k_dense(const __grid_constant__
     tc::tmem_dealloc_pair(tmem, 2 * BN);
   }
 }
+
+// ------------------------------------------------------------ tokens as columns
+// The same pairs the other way round: 256 weight rows are the MMA's rows (128 in each
+// CTA's TMEM lanes), up to 512 tokens its columns, in one or two accumulators of `nacc`
+// tokens.  A tile's tokens are then no more than there are (rounded up to 32 or 64), where
+// tiles of 256 tokens would leave part of the last one empty, and a weight row is
+// fetched once for all of them.  In the gated product a CTA's 128 rows are 64 of w_gate and
+// the same 64 of w_up.  A pair has one tile.  Its sums go to shared memory, which the
+// operands need no more, and from there out, four features of a token a thread.
+struct ColumnsParams {
+  CUtensorMap x_map;          // x [T][K], box 64 x nacc / 2
+  CUtensorMap w_map, w2_map;  // weights [F][K], box 64 x 128 (gated: 64)
+  FusedParams f;
+  int KB;                     // K steps of 128
+  int nacc, accs;             // tokens of an accumulator, accumulators
+  int stages;
+  int vec_r, vec_y;           // residual and y rows are whole 16-byte units
+  int32_t* err;
+};
+constexpr int CL_MAXST = 6;
+
+template <bool GATED, int ACT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DN_THREADS, 1)
+    k_columns(const __grid_constant__ ColumnsParams P) {
+  constexpr int FT = GATED ? 64 : 128;  // features of a CTA
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* base = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int N = P.nacc * P.accs;
+  const int x_bytes = 64 * P.nacc;                       // an accumulator's tokens, 64 of K
+  const int half_bytes = DN_A_BYTES + P.accs * x_bytes;  // 64 of K
+  const int stage = 2 * half_bytes;
+  struct Bars {
+    uint64_t full[CL_MAXST], empty[CL_MAXST], tfull;
+    uint32_t tmem_base;
+    volatile int failed;
+  };
+  Bars& B = *reinterpret_cast<Bars*>(base + P.stages * stage);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int rank = tc::cluster_rank();
+  const int f0 = FT * blockIdx.x;  // the CTA's first feature
+
+  if (threadIdx.x == 32 * 8) {
+    // launch arguments: no earlier kernel writes them
+    tc::prefetch_map(&P.x_map);
+    tc::prefetch_map(&P.w_map);
+    if (GATED) tc::prefetch_map(&P.w2_map);
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < P.stages; ++s) {
+      mbar_init(&B.full[s], 1);
+      mbar_init(&B.empty[s], 1);
+    }
+    mbar_init(&B.tfull, 1);
+    B.failed = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) tc::tmem_alloc_pair(&B.tmem_base, 512);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::cluster_sync();
+  tc::fence_after_sync();
+  grid_dep_wait();  // nothing above touched the operands
+  grid_dep_trigger();
+  const uint32_t tmem = B.tmem_base;
+
+  if (warp == 8) {
+    if (tc::elect_one()) {
+      int s = 0;
+      uint32_t phase = 1;
+      const uint32_t full = tc::map_to_rank(&B.full[0], 0);
+      for (int kb = 0; kb < P.KB; ++kb) {
+        if (!mbar_wait(&B.empty[s], phase, P.err)) {
+          B.failed = 1;
+          break;
+        }
+        const uint32_t fb = full + 8 * s;
+        const int parts = 128 * kb + 64 < P.f.K ? 2 : 1;
+        if (rank == 0) mbar_arrive_expect_tx(&B.full[s], (uint32_t)(2 * parts * half_bytes));
+        for (int part = 0; part < parts; ++part) {
+          unsigned char* at = base + (size_t)s * stage + part * half_bytes;
+          const int k = 128 * kb + 64 * part;
+          tc::tma_load_2d_pair(at, &P.w_map, k, f0, fb);
+          if (GATED) tc::tma_load_2d_pair(at + DN_A_BYTES / 2, &P.w2_map, k, f0, fb);
+          for (int a = 0; a < P.accs; ++a)
+            tc::tma_load_2d_pair(at + DN_A_BYTES + a * x_bytes, &P.x_map, k,
+                                 P.nacc * a + P.nacc / 2 * rank, fb);
+        }
+        if (++s == P.stages) s = 0, phase ^= 1;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    if (rank == 0 && tc::elect_one()) {
+      const uint32_t id = tc::idesc_bf16(256, P.nacc, false, false);
+      const uint64_t a_desc = tc::desc_sw128(smem_u32(base), 16, 1024);
+      int s = 0;
+      uint32_t phase = 0;
+      for (int kb = 0; kb < P.KB; ++kb) {
+        if (!mbar_wait(&B.full[s], phase, P.err)) {
+          B.failed = 1;
+          break;
+        }
+        tc::fence_after_sync();
+        const int parts = 128 * kb + 64 < P.f.K ? 2 : 1;
+        for (int part = 0; part < parts; ++part) {
+          const uint64_t a = a_desc + (uint64_t)((s * stage + part * half_bytes) >> 4);
+          for (int acc = 0; acc < P.accs; ++acc) {
+            const uint64_t x = a + ((DN_A_BYTES + acc * x_bytes) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc::mma_pair_bf16(tmem + P.nacc * acc, a + 2 * kk, x + 2 * kk, id,
+                                (kb > 0 || part > 0 || kk > 0) ? 1u : 0u);
+          }
+        }
+        tc::commit_pair_to(&B.empty[s], 3);
+        if (++s == P.stages) s = 0, phase ^= 1;
+      }
+      tc::commit_pair_to(&B.tfull, 3);
+    }
+    __syncwarp();
+  }
+  // every warp: the products are done with the operands
+  bool ok = mbar_wait(&B.tfull, 0, P.err) && !B.failed;
+  ok = __syncthreads_and(ok);
+  tc::fence_after_sync();
+  float* sums = reinterpret_cast<float*>(base);  // [token][128]
+  const int most = P.stages * stage / 512 / 32 * 32;
+  const int tokens = min(N, P.f.T);
+  for (int t0 = 0; ok && t0 < tokens; t0 += most) {
+    const int end = min(tokens, t0 + most);
+    if (warp < 8) {
+      const int quad = warp & 3;
+#pragma unroll 1
+      for (int c = t0 + 32 * (warp >> 2); c < end; c += 64) {
+        uint32_t r[32];
+        tc::tmem_ld32(tmem + ((uint32_t)(32 * quad) << 16) + c, r);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          sums[128 * (c - t0 + i) + 32 * quad + lane] = __uint_as_float(r[i]);
+      }
+    }
+    __syncthreads();
+    constexpr int GR = FT / 4;
+    const int c4 = threadIdx.x % GR, f = f0 + 4 * c4;
+    if (threadIdx.x < DN_EPI && f < P.f.F) {
+      const int el = P.f.f32 ? 4 : 2;
+      const bool vec = f + 4 <= P.f.F && P.vec_y && (!P.f.residual || P.vec_r);
+      float bias[4] = {};
+      if (!GATED && P.f.bias)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (f + j < P.f.F) bias[j] = bf1(P.f.bias[f + j]);
+#pragma unroll 4
+      for (int t = t0 + threadIdx.x / GR; t < end; t += DN_EPI / GR) {
+        float4 v = *reinterpret_cast<const float4*>(sums + 128 * (t - t0) + 4 * c4);
+        v.x = activate(v.x + bias[0], ACT), v.y = activate(v.y + bias[1], ACT);
+        v.z = activate(v.z + bias[2], ACT), v.w = activate(v.w + bias[3], ACT);
+        if (GATED) {
+          const float4 u = *reinterpret_cast<const float4*>(sums + 128 * (t - t0) + 64 + 4 * c4);
+          v.x *= u.x, v.y *= u.y, v.z *= u.z, v.w *= u.w;
+        }
+        finish_four(P.f, el, vec, t, f, v);
+      }
+    }
+    __syncthreads();
+  }
+  if (!ok) {
+    B.failed = 1;
+    // a wait gave up: give copies that may still be in flight time to land
+    const uint64_t tw = globaltimer_ns();
+    while (globaltimer_ns() - tw < kDrainNs) {
+    }
+  }
+  tc::fence_before_sync();
+  tc::cluster_sync();  // nothing of the pair's reads this CTA's memory any more
+  if (warp == 9) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+using ColumnsKernel = void (*)(const ColumnsParams);
+const ColumnsKernel kColumns[2][4] = {
+    {k_columns<false, 0>, k_columns<false, 1>, k_columns<false, 2>, k_columns<false, 3>},
+    {k_columns<true, 0>, k_columns<true, 1>, k_columns<true, 2>, k_columns<true, 3>}};
 
 using DenseKernel = void (*)(const DenseParams);
 // [gated 256, 256, 128][activation]
@@ -738,6 +931,11 @@ int dense_attributes(Room& room) {
       if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, DN_SMEM) !=
           cudaSuccess)
         return ER_ECUDA;
+  for (auto& row : kColumns)
+    for (ColumnsKernel fn : row)
+      if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, DN_SMEM) !=
+          cudaSuccess)
+        return ER_ECUDA;
   for (int S = 1; S <= 4; ++S) {
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = dense_config(attr, 1, S, nullptr);
@@ -752,39 +950,86 @@ int dense_attributes(Room& room) {
   return ER_OK;
 }
 
+// How a product is cut: tiles of 256 tokens by BN weight rows, K in S shares; or (BN = 0)
+// tiles of 256 weight rows by `accs` times `nacc` tokens.
 struct DensePlan {
   int BN, S, clusters;
+  int nacc, accs;
 };
 
-// The tile width and the shares of K, by the estimated cycles of a pair.  A K step
-// costs the longer of its MMAs (4 BN cycles) and its fetches (measured: one SM's TMA
-// brings about 60 bytes per cycle in these boxes); joining shares costs the copies
-// between the CTAs (measured: 16 bytes per cycle into a CTA) and two more barriers of
-// the cluster.
+// The cut with the least estimated cycles of a pair.  A K step of 128 costs the longer of
+// its MMAs (4 cycles a column) and its fetches (measured: one SM's TMA brings about 60
+// bytes per cycle in these boxes, about 24 of weights that come from HBM); joining shares
+// costs the copies between the CTAs (measured: 16 bytes per cycle into a CTA) and two more
+// barriers of the cluster; an epilogue that nothing runs beside about 12 cycles a column.
 DensePlan choose_plan(int T, int F, int K, bool gated, const Room& room) {
   const int KB = (K + 127) / 128, n_m = (T + 255) / 256, rows = T < 128 ? T : 128;
-  DensePlan best{256, 1, 1};
+  const auto step = [](double columns, double bytes, double weights, bool once) {
+    const double mma = 4.0 * columns, fetch = bytes / 60.0, hbm = once ? weights / 24.0 : 0.0;
+    return mma > fetch ? (mma > hbm ? mma : hbm) : (fetch > hbm ? fetch : hbm);
+  };
+  DensePlan best{256, 1, 1, 0, 0};
   double least = 1e300;
   for (int BN : {256, 128}) {
     if (gated && BN != 256) continue;
     const int FT = gated ? BN / 2 : BN, tiles = n_m * ((F + FT - 1) / FT);
     for (int S = 1; S <= 4 && S <= KB; ++S) {
       if (S > 1 && tiles > room.clusters[S]) break;
-      const double mma = 4.0 * BN, fetch = (256.0 * rows + 128.0 * BN) / 60.0;
       const int clusters = tiles < room.clusters[S] ? tiles : room.clusters[S];
       const int waves = (tiles + clusters - 1) / clusters;
       const double join = 4000.0 + 4.0 * BN * rows * (S - 1) / S / 16.0;
-      const double cost =
-          waves * ((KB + S - 1) / S) * (mma > fetch ? mma : fetch) + (S > 1 ? join : 1500.0);
+      const double cost = waves * ((KB + S - 1) / S) *
+                              step(BN, 256.0 * rows + 128.0 * BN, 128.0 * BN, n_m == 1) +
+                          (S > 1 ? join : 12.0 * BN);
       if (cost < least) {
         least = cost;
-        best = DensePlan{BN, S, clusters};
+        best = DensePlan{BN, S, clusters, 0, 0};
       }
     }
+  }
+  const int accs = T > 256 ? 2 : 1, nacc = ((T + accs - 1) / accs + 31) / 32 * 32;
+  const int tiles = (F + (gated ? 127 : 255)) / (gated ? 128 : 256);
+  if (T > FV_TOKENS && T <= 512 && tiles <= room.clusters[1]) {
+    const int N = nacc * accs;
+    const double cost = KB * step(N, 32768.0 + 128.0 * N, 32768.0, true) + 2000.0 + 12.0 * N;
+    if (cost < least) best = DensePlan{0, 1, tiles, nacc, accs};
   }
   return best;
 }
 
+int launch_columns(const FusedParams& F, const DensePlan& plan, int32_t* err, cudaStream_t st) {
+  const bool gated = F.w2 != nullptr;
+  ColumnsParams P{};
+  P.f = F;
+  P.err = err;
+  P.nacc = plan.nacc;
+  P.accs = plan.accs;
+  P.KB = (F.K + 127) / 128;
+  const int stage = 2 * (DN_A_BYTES + 64 * plan.nacc * plan.accs);
+  P.stages = (DN_SMEM - 2048) / stage;
+  if (P.stages > CL_MAXST) P.stages = CL_MAXST;
+  const int el = F.f32 ? 4 : 2;
+  P.vec_r = aligned16(F.residual) && F.ldr * el % 16 == 0;
+  P.vec_y = aligned16(F.y) && F.ldy * el % 16 == 0;
+  const int box = gated ? 64 : 128;
+  if (!encode_rows(&P.x_map, F.x, false, F.K, F.T, F.ldx * 2, 64, plan.nacc / 2) ||
+      !encode_rows(&P.w_map, F.w, false, F.K, F.F, (uint64_t)F.K * 2, 64, box) ||
+      (gated && !encode_rows(&P.w2_map, F.w2, false, F.K, F.F, (uint64_t)F.K * 2, 64, box)))
+    return ER_ECUDA;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * plan.clusters);
+  cfg.blockDim = dim3(DN_THREADS);
+  cfg.dynamicSmemBytes = DN_SMEM;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kColumns[gated ? 1 : 0][F.act], P) != cudaSuccess) return ER_ECUDA;
+  count_launches(1);
+  return launch_status();
+}
 
 int launch_dense(const FusedParams& F, int32_t* err, cudaStream_t st) {
   const bool gated = F.w2 != nullptr;
@@ -792,6 +1037,7 @@ int launch_dense(const FusedParams& F, int32_t* err, cudaStream_t st) {
   const int rc = dense_attributes(room);
   if (rc != ER_OK) return rc;
   const DensePlan plan = choose_plan(F.T, F.F, F.K, gated, room);
+  if (plan.BN == 0) return launch_columns(F, plan, err, st);
   DenseParams P{};
   P.f = F;
   const int FT = gated ? plan.BN / 2 : plan.BN;

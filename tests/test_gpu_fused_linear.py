@@ -83,7 +83,10 @@ SIZES = [(1, 2560, 4096), (1, 1, 8), (2, 3, 16), (5, 63, 72), (8, 4099, 2568), (
          (16, 2560, 2560), (17, 96, 1000), (31, 1025, 136), (32, 256, 64), (33, 2560, 4096),
          (64, 777, 520), (100, 2561, 96), (127, 128, 2560), (128, 2560, 4096), (129, 511, 192),
          (200, 3000, 328), (255, 257, 1032), (256, 256, 256), (300, 1100, 2560), (385, 520, 72),
-         (512, 2560, 4096), (700, 1411, 200), (1025, 2560, 640), (2050, 333, 136)]
+         (512, 2560, 4096), (700, 1411, 200), (1025, 2560, 640), (2050, 333, 136),
+         # wide products of a few hundred tokens (tokens as columns), odd ones among them
+         (260, 19000, 136), (300, 9000, 264), (301, 18945, 72), (512, 18944, 200),
+         (513, 9601, 136), (700, 19001, 72), (100, 9473, 520), (9, 18945, 264), (33, 9500, 72)]
 
 
 @pytest.mark.parametrize("T,F,K", SIZES)
