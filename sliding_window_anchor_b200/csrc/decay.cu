@@ -347,7 +347,10 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     int anybad[4];
     uint64_t k_full[2], k_empty[2], v_full[3], v_empty[3], gate_full[2], gate_empty[2];
     uint64_t vt_empty[2], last;  // STATES
-    uint64_t o_full, o_empty[2], q_full, q_empty, p_full, pt_full, vt_full, s_full, sb_full, done;
+    // one for each buffer of Ṽ: with one for both, a warp that is a chunk ahead would count
+    // for one that is not there yet
+    uint64_t vt_full[2];
+    uint64_t o_full, o_empty[2], q_full, q_empty, p_full, pt_full, s_full, sb_full, done;
     double g_total;
     Item item;
     uint32_t tmem_base;
@@ -389,7 +392,8 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     mbar_init(&B.q_empty, 1);
     mbar_init(&B.p_full, 1);
     mbar_init(&B.pt_full, 10);
-    mbar_init(&B.vt_full, 8);
+    mbar_init(&B.vt_full[0], 8);
+    mbar_init(&B.vt_full[1], 8);
     mbar_init(&B.s_full, 1);
     mbar_init(&B.sb_full, 4);
     mbar_init(&B.done, 1);
@@ -515,7 +519,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
           }
           // S += Kᵀ Ṽ, its three terms side by side (K is read once; with k_dim 64, lanes
           // 64.. take v's rows for columns of k: never read)
-          ok = wait_bar(&B.vt_full, c, D.err);
+          ok = wait_bar(&B.vt_full[c & (NV - 1)], c / NV, D.err);
           if (!ok) break;
           tc::fence_after_sync();
           const uint64_t terms = vt_desc + (c & (NV - 1)) * (3 * VB / 16);
@@ -713,7 +717,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         }
         if (odd & 0x7FFF7FFFu) mark_row(v, to, sw, half, j, B.colbad[c & 3], &B.anybad[c & 3]);
         tc::fence_async_smem();
-        arrive(&B.vt_full);
+        arrive(&B.vt_full[c & (NV - 1)]);
         if (lane == 0) {
           mbar_arrive(&B.gate_empty[s]);
           if (STATES) mbar_arrive(&B.v_empty[vs]);

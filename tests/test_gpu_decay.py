@@ -310,6 +310,25 @@ def test_captured_calls_and_streams(sab, lengths):
     assert all(torch.equal(x, want) for x in got)
 
 
+@pytest.mark.parametrize("lengths,heads", [([16000], (8, 16, 128, 128)),
+                                           ([900, 33, 2000], (4, 8, 64, 64))])
+def test_many_calls_in_a_row(sab, lengths, heads):
+    """Calls behind one another, enough of them for a warp that runs ahead of another to
+    show: every one gives the same bits, and no wait gives up."""
+    c = Case(lengths, *heads)
+    want_s = c.state.clone()
+    want = sab.decay_prefill(want_s, c.ids, c.cu, c.q, c.k, c.v, c.g)
+    states = [c.state.clone() for _ in range(4)]
+    for _ in range(40):
+        for s in states:
+            s.copy_(c.state)
+        outs = [sab.decay_prefill(s, c.ids, c.cu, c.q, c.k, c.v, c.g) for s in states]
+        assert all(torch.equal(s, want_s) for s in states)
+        assert all(torch.equal(o, want) for o in outs)
+    assert sab.last_call_error() == 0
+    c.check(want, want_s)
+
+
 def test_offsets_past_32_bits(sab):
     """State rows, and token rows, more than 2^31 elements from the first."""
     rows = 2 ** 31 // (32 * 128 * 128) + 3
