@@ -294,9 +294,10 @@ int er_linear(const er_bf16* x, int32_t T, const er_bf16* w, int32_t F, int32_t 
  * bias, activation, gate product and residual are FP32 and rounded once, into
  * y.  Activations: ER_ACT_*.
  *  T >= 0 (0: nothing is enqueued), F >= 1, K >= 8 and a multiple of 8, each at
- *  most 2^30, ldx >= K and a multiple of 8, ldy and ldr >= F; x, w, w_gate, w_up 16-byte aligned, the
- *  other pointers aligned to their elements; y overlaps no input but a residual
- *  equal to it.  Columns from F on of y are left as they are.  No workspace.
+ *  most 2^30, ldx >= K and a multiple of 8, ldy and ldr >= F; x, w, w_gate, w_up
+ *  16-byte aligned, the other pointers aligned to their elements; y overlaps no
+ *  input but a residual equal to it (an input that starts where y starts is
+ *  refused).  Columns from F on of y are left as they are.  No workspace.
  *  The summation order is fixed for given sizes and alignments: the same inputs
  *  give the same bits.  A bounded wait that gives up records ER_ETIMEOUT in
  *  *dev_error (NULL: the library's own word, er_last_call_error).
@@ -329,21 +330,27 @@ int er_gated_linear(const er_bf16* x, int32_t ldx, int32_t T, const er_bf16* w_g
  *   log_decay FP32 rows of [v_heads] natural logs, ldg apart, or ldg = 0: one
  *          row for every token.  Any value but +inf: 0 keeps the state, -inf
  *          forgets it (so does every value below -150), NaN spreads as in the
- *          formula.
+ *          formula.  So do infinite and NaN values of q, k and v: nothing
+ *          in front of their token depends on them (an infinite k or v
+ *          may leave NaN for an infinity).
  *   o      BF16 rows of [v_heads][v_dim], ldo apart, rounded once.
  * er_decay_decode: one token for each of B sequences, row b the token of
  * sequence b.  er_decay_prefill: the tokens of sequence b are rows
  * [cu_tokens[b], cu_tokens[b + 1]) (device int32 [B + 1]) of T packed rows;
  * empty sequences keep their state; rows outside every sequence are left as
  * they are in o.  A sequence's tokens may be cut into calls anywhere.
- *  v_heads a multiple of k_heads, at most 4096; k_dim, v_dim 64 or 128; 0 <= B <=
- *  s_max (larger: ER_ECAPACITY), B <= 65535; row strides multiples of 8 and at
- *  least a row; state, q, k, v, o 16-byte aligned; ws 256-byte aligned, at least
- *  er_decay_prefill_workspace_bytes(shape, B, T) (0 for bad sizes).  o overlaps no
- *  input.  A sequence whose state row is out of range or was listed before it in
- *  the call, or whose rows leave [0, T), is skipped (its state and its rows of
- *  o are left as they are) and records ER_EINVAL in *dev_error (NULL: the library's
- *  own word, er_last_call_error).  The same inputs give the same bits. */
+ *  v_heads a multiple of k_heads, at most 4096; k_dim, v_dim 64 or 128;
+ *  0 <= B <= s_max (larger: ER_ECAPACITY), B <= 65535, T <= 2^30; row strides
+ *  multiples of 8 and at least a row; state, q, k, v, o 16-byte aligned; ws
+ *  256-byte aligned, at least er_decay_prefill_workspace_bytes(shape, B, T) (for
+ *  the current device; 0 for bad sizes).  o overlaps no input (one that starts
+ *  where o starts is refused); calls in flight at the same time share no workspace
+ *  and no state row.
+ *  A sequence whose state row is out of range or was listed before it in the
+ *  call, or whose rows leave [0, T), is skipped (its state and its rows of o are
+ *  left as they are) and records ER_EINVAL in *dev_error (NULL: the library's own
+ *  word, er_last_call_error); so are sequences past the first T tokens of a
+ *  call.  The same inputs give the same bits. */
 typedef struct er_decay_shape {
   int32_t k_heads, v_heads, k_dim, v_dim;
 } er_decay_shape;

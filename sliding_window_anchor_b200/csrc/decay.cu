@@ -52,7 +52,8 @@ __device__ __forceinline__ bool sequence_rows(const DecayParams& P, int b, int& 
 // One block per (sequence, value head, COLS columns of its state): the state streams
 // through registers once, 16 bytes a thread and row; every thread's rows are
 // requested before the first is used.  o's sums over the rows are joined in a fixed
-// order.
+// order.  HBM bounds it: 512 sequences of 32 heads of 128 x 128 take 344 us (2.2 GB read
+// and written: 6.3 TB/s, 0.97 of a plain copy).
 constexpr int DD_THREADS = 256;
 
 template <int DK, int COLS>
@@ -164,6 +165,15 @@ int launch_decode(const DecayParams& P, cudaStream_t st) {
 // what the segments in front of each leave together, which its walk starts from.  There a
 // segment's chunks are walked from its end, so that all decays are known and no
 // product waits for another.
+//
+// What bounds it: 32768 tokens of 32 heads of 128 x 128 (16 of q and k) take 535 us: STATES
+// 165, the join 10, the walk 340.  A walk's chunk takes about 4800 cycles: two
+// chains (Q Kᵀ - decayed - times V, and the state out of TMEM - Q S - Kᵀ Ṽ) that meet in
+// every chunk, each a row of waits of some hundred cycles, over 400 KB of shared-memory
+// traffic (3100 cycles); a chunk of STATES takes 2040, the latency of its decays' sums.
+// The tensor cores are busy 16-25%.  Chunks of 64 tokens would have the same waits for half of
+// the tokens; slices of 128 columns have no room beside two chunks of k and v in shared
+// memory and three terms of the state in TMEM.
 //
 // Warps, by the TMEM lanes (32 · (warp % 4)..) that they can reach and by warp / 4: below
 // warp / 4 = 4 one for each block of 32 x 32 of Q Kᵀ on and below the diagonal (lanes
@@ -1060,7 +1070,8 @@ int fill(DecayParams& P, float* state, int32_t s_max, const int32_t* seq_ids, co
   if (B == 0) return ER_OK;
   if (!state || !seq_ids || !aligned16(state) || ((uintptr_t)seq_ids & 3u)) return ER_EINVAL;
   if (T > 0 && (!q || !k || !v || !g || !o || !aligned16(q) || !aligned16(k) || !aligned16(v) ||
-                !aligned16(o) || ((uintptr_t)g & 3u)))
+                !aligned16(o) || ((uintptr_t)g & 3u) || o == q || o == k || o == v ||
+                (void*)o == state || (const void*)o == g))
     return ER_EINVAL;
   P = DecayParams{state, s_max, seq_ids, cu, B, T, sh->k_heads, sh->v_heads, sh->k_dim, sh->v_dim,
                   q, k, v, ldq, ldk, ldv, ldg, ldo, g, scale, o, dev_error};

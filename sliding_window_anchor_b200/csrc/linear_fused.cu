@@ -180,7 +180,9 @@ __device__ __forceinline__ void copy_rows(const FusedParams& P, const unsigned c
 // rows (rows g and g + 8, columns 8c..8c+7 of the step, g = lane/4, c = lane%4)
 // and 16 bytes of token g, and feeds them unchanged to two m16n8k16 products
 // (a K column meets the same K column on both operands, so their order does not
-// matter).  The K slices of a block's warps are added in a fixed order.
+// matter).  The K slices of a block's warps are added in a fixed order.  HBM bounds it:
+// 1 x 2560 x 4096 takes 7.4 us (2.8 TB/s; launch and ramp are half of it), gated
+// 1 x 2*6912 x 2560 14-18 us (70.8 MB; 4.0-4.9 TB/s).
 constexpr int FV_TOKENS = 8;
 constexpr int FV_MAXW = 8;
 
@@ -313,6 +315,12 @@ int launch_few(const FusedParams& P, cudaStream_t st) {
 // (few tiles): the pairs of a cluster each take a share of K of the cluster's
 // one tile, leave their FP32 sums in shared memory, and each adds up a part of
 // the tile over distributed shared memory, in the order of the shares.
+//
+// The tensor cores bound large products: 8192 x 10240 x 2560 takes 280 us (1.53 PFLOP/s;
+// the library's product alone 277), gated 4096 x 2*10240 x 2560 284.  Middling ones are
+// bound by what surrounds the tile: of 512 x 2560 x 4096 (17.2 us) 6.5 us are its
+// products at the tensor cores' rate; the launch, the ring's first fill from HBM, the
+// joining of the shares and the epilogue follow one another around them.
 //
 // Per CTA: warp 8 — TMA; warp 9 — TMEM and, in a pair's even CTA, the MMAs;
 // warps 0-7 — the epilogue: warp w has the TMEM lanes (tokens) of quadrant w % 4
@@ -704,7 +712,9 @@ __global__ void __launch_bounds__(DN_THREADS, 1) k_dense(const __grid_constant__
 // tiles of 256 tokens would leave part of the last one empty, and a weight row is
 // fetched once for all of them.  In the gated product a CTA's 128 rows are 64 of w_gate and
 // the same 64 of w_up.  A pair has one tile.  Its sums go to shared memory, which the
-// operands need no more, and from there out, four features of a token a thread.
+// operands need no more, and from there out, four features of a token a thread.  The weights'
+// stream and the tensor cores bound it about alike: gated 300 x 2*9000 x 2560 takes 27 us
+// (tiles of 256 tokens: 35; 92 MB of weights at 3.4 TB/s, 1.0 PFLOP/s).
 struct ColumnsParams {
   CUtensorMap x_map;          // x [T][K], box 64 x nacc / 2
   CUtensorMap w_map, w2_map;  // weights [F][K], box 64 x 128 (gated: 64)
@@ -1074,8 +1084,9 @@ int launch_fused(const FusedParams& P, int32_t* err, cudaStream_t st) {
 bool sizes_ok(int32_t T, int32_t F, int32_t K, int32_t ldx, int32_t act, int32_t y_fp32,
               int32_t ldy) {
   constexpr int32_t kMost = 1 << 30;  // tile corners stay within 32 bits
-  return T >= 0 && T <= kMost && F >= 1 && F <= kMost && K >= 8 && K <= kMost && K % 8 == 0 && ldx >= K && ldx % 8 == 0 && ldy >= F &&
-         act >= ER_ACT_NONE && act <= ER_ACT_GELU_TANH && (y_fp32 == 0 || y_fp32 == 1);
+  return T >= 0 && T <= kMost && F >= 1 && F <= kMost && K >= 8 && K <= kMost && K % 8 == 0 &&
+         ldx >= K && ldx % 8 == 0 && ldy >= F && act >= ER_ACT_NONE &&
+         act <= ER_ACT_GELU_TANH && (y_fp32 == 0 || y_fp32 == 1);
 }
 
 }  // namespace
@@ -1093,7 +1104,8 @@ int er_linear_fused(const er_bf16* x, int32_t ldx, int32_t T, const er_bf16* w, 
   if (T == 0) return ER_OK;
   const uintptr_t el = y_fp32 ? 3u : 1u;
   if (!x || !w || !y || !aligned16(x) || !aligned16(w) || ((uintptr_t)y & el) ||
-      ((uintptr_t)residual & el) || ((uintptr_t)bias & 1u))
+      ((uintptr_t)residual & el) || ((uintptr_t)bias & 1u) || y == x || y == w || y == bias ||
+      (residual == y && ldr != ldy && T > 1))
     return ER_EINVAL;
   FusedParams P{x, w, nullptr, bias, residual, y, T, F, K, ldx, ldr, ldy, act, y_fp32};
   int32_t* err = dev_error ? dev_error : call_error_word();
@@ -1107,7 +1119,7 @@ int er_gated_linear(const er_bf16* x, int32_t ldx, int32_t T, const er_bf16* w_g
   if (!sizes_ok(T, F, K, ldx, act, y_fp32, ldy)) return ER_EINVAL;
   if (T == 0) return ER_OK;
   if (!x || !w_gate || !w_up || !y || !aligned16(x) || !aligned16(w_gate) || !aligned16(w_up) ||
-      ((uintptr_t)y & (y_fp32 ? 3u : 1u)))
+      ((uintptr_t)y & (y_fp32 ? 3u : 1u)) || y == x || y == w_gate || y == w_up)
     return ER_EINVAL;
   FusedParams P{x, w_gate, w_up, nullptr, nullptr, y, T, F, K, ldx, 0, ldy, act, y_fp32};
   int32_t* err = dev_error ? dev_error : call_error_word();

@@ -5,7 +5,7 @@ import ctypes
 import pytest
 import torch
 
-OK = 1 << 40          # an aligned address that nothing reads
+OK, W, Y, S, V = (n << 40 for n in range(1, 6))  # aligned addresses that nothing reads
 ODD = (1 << 40) + 2   # aligned to two bytes only
 BIG = 1 << 30
 
@@ -24,9 +24,9 @@ def unlaunched(L):
     assert L.er_launch_count() == before
 
 
-LINEAR = dict(x=OK, ldx=64, T=4, w=OK, F=24, K=64, bias=None, act=0, residual=None, ldr=24, y=OK,
+LINEAR = dict(x=OK, ldx=64, T=4, w=W, F=24, K=64, bias=None, act=0, residual=None, ldr=24, y=Y,
               y_fp32=0, ldy=24, dev_error=None, stream=None)
-GATED = dict(x=OK, ldx=64, T=4, w_gate=OK, w_up=OK, F=24, K=64, act=1, y=OK, y_fp32=0, ldy=24,
+GATED = dict(x=OK, ldx=64, T=4, w_gate=W, w_up=W, F=24, K=64, act=1, y=Y, y_fp32=0, ldy=24,
              dev_error=None, stream=None)
 
 
@@ -35,7 +35,7 @@ GATED = dict(x=OK, ldx=64, T=4, w_gate=OK, w_up=OK, F=24, K=64, act=1, y=OK, y_f
     dict(ldx=68), dict(ldy=23), dict(act=4), dict(act=-1), dict(y_fp32=2), dict(x=None),
     dict(w=None), dict(y=None), dict(x=ODD), dict(w=ODD), dict(y=ODD, y_fp32=1), dict(y=OK + 1),
     dict(residual=OK, ldr=23), dict(residual=OK + 1), dict(residual=ODD, y_fp32=1),
-    dict(bias=OK + 1)])
+    dict(bias=OK + 1), dict(y=OK), dict(y=W), dict(bias=Y), dict(residual=Y, ldr=32)])
 def test_linear_fused_refuses(unlaunched, change):
     assert unlaunched.er_linear_fused(*{**LINEAR, **change}.values()) == -1
 
@@ -43,7 +43,7 @@ def test_linear_fused_refuses(unlaunched, change):
 @pytest.mark.parametrize("change", [
     dict(T=-1), dict(F=0), dict(K=12), dict(ldx=60), dict(ldy=20), dict(act=9), dict(y_fp32=-1),
     dict(x=None), dict(w_gate=None), dict(w_up=None), dict(y=None), dict(x=ODD), dict(w_gate=ODD),
-    dict(w_up=ODD), dict(y=OK + 1), dict(y=ODD, y_fp32=1)])
+    dict(w_up=ODD), dict(y=OK + 1), dict(y=ODD, y_fp32=1), dict(y=OK), dict(y=W), dict(w_up=Y)])
 def test_gated_linear_refuses(unlaunched, change):
     assert unlaunched.er_gated_linear(*{**GATED, **change}.values()) == -1
 
@@ -59,8 +59,8 @@ def shape(*dims):
 
 
 def decay_args(prefill, **change):
-    a = dict(state=OK, s_max=8, seq_ids=OK, cu=OK, B=4, T=100, sh=(2, 4, 64, 128), q=OK, ldq=128,
-             k=OK, ldk=128, v=OK, ldv=512, g=OK, ldg=4, scale=1.0, o=OK, ldo=512, ws=OK,
+    a = dict(state=S, s_max=8, seq_ids=OK, cu=OK, B=4, T=100, sh=(2, 4, 64, 128), q=OK, ldq=128,
+             k=OK, ldk=128, v=V, ldv=512, g=OK, ldg=4, scale=1.0, o=Y, ldo=512, ws=OK,
              ws_bytes=BIG, dev_error=None, stream=None)
     assert set(change) <= set(a)
     a.update(change)
@@ -78,7 +78,7 @@ BAD_DECAY = [dict(s_max=0), dict(B=-1), dict(B=65536, s_max=70000), dict(sh=None
              dict(ldv=504), dict(ldv=516), dict(ldo=8), dict(ldo=514), dict(ldg=3), dict(ldg=-4),
              dict(state=None), dict(seq_ids=None), dict(q=None), dict(k=None), dict(v=None),
              dict(g=None), dict(o=None), dict(state=ODD), dict(q=ODD), dict(k=ODD), dict(v=ODD),
-             dict(o=ODD), dict(g=ODD), dict(seq_ids=ODD)]
+             dict(o=ODD), dict(g=ODD), dict(seq_ids=ODD), dict(o=OK), dict(o=V), dict(o=S)]
 
 
 @pytest.mark.parametrize("change", BAD_DECAY)

@@ -3,8 +3,8 @@ er_decay_prefill) with the recurrence in float64, token by token.
 
 Bars, per element.  Beside the state S runs A = e^g A + |k| |v|ᵀ (from |S_0|), the sum of
 the terms' sizes, and beside o runs m = |scale| · Aᵀ |q|:
-  state: every term is rounded in two BF16 parts (2^-16 of it is lost at most), decayed by
-    a few FP32 exponentials and summed in FP32: |Δ| <= 2^-15·A;
+  state: every term enters as BF16 parts (of two, 2^-16 is lost at most; the kernel takes
+    three), decayed by a few FP32 exponentials and summed in FP32: |Δ| <= 2^-15·A;
   o: each term meets one BF16 rounding on its way (of the masked q·k product, or of the
     state it is read from), 2^-8 of it, and the sum is rounded once:
     |Δ| <= (2^-8 + 2^-14)·m + 2^-8·|o|.
