@@ -7,6 +7,7 @@
 //
 // per value head, S FP32 [k_dim][v_dim]; value head h reads the q and k of head
 // h / (v_heads / k_heads).
+#include <algorithm>
 #include <mutex>
 
 #include "common.cuh"
@@ -28,6 +29,10 @@ struct DecayParams {
   float scale;
   uint16_t* o;
   int32_t* err;
+  // prompts: sequences of `few` tokens and fewer are k_decay_few's, the segments of L tokens of
+  // longer ones k_decay_chunks'; *items: these segments' number at most (NULL: not known)
+  int few, L;
+  int32_t* items;
 };
 
 // The rows [begin, end) of sequence b; false when its state row or its rows
@@ -146,6 +151,183 @@ int launch_decode(const DecayParams& P, cudaStream_t st) {
                     blocks, DD_THREADS, P, st);
 }
 
+// ------------------------------------------------------------ short sequences
+// As for single tokens, with a loop over the sequence's tokens while the state is in registers:
+// the state is read and written once, whatever their number.  A thread's rows follow one
+// another; k and q of four tokens are in shared memory as pairs of equal values, for
+// products on pairs of columns (fma.f32x2), while the next four tokens' rows are on their
+// way.  HBM bounds it for few tokens (512 sequences of 4, 32 heads of 128 x 128: 480 us, of
+// 1: 350), the FP32 products from about 8 on (of 16: 970): three for each value of the state
+// and token.  Eight columns a thread, with half of the fetches from shared memory, took
+// longer (550 and 1130 us).
+constexpr int DF_TOKENS = 4;  // between two barriers
+
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair_of(float lo, float hi) {
+  f32x2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 halves(f32x2 d) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(d));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from)
+                 : "memory");
+}
+
+template <int DK, int COLS>
+__global__ void __launch_bounds__(DD_THREADS, 2) k_decay_few(const DecayParams P) {
+  constexpr int LN = COLS / 4;         // threads of a row
+  constexpr int RP = DD_THREADS / LN;  // threads of a column
+  constexpr int N = DK / RP;           // rows of a thread
+  constexpr int WARPS = DD_THREADS / 32;
+  static_assert(N >= 2 && N % 2 == 0, "");
+  __shared__ __align__(16) f32x2 qs[DF_TOKENS][DK], ks[DF_TOKENS][DK];
+  __shared__ __align__(16) uint16_t raw[2][DF_TOKENS][2 * DK + COLS];  // q, k and v
+  __shared__ float log_decay[2][DF_TOKENS];
+  __shared__ float4 part[DF_TOKENS][WARPS][LN];
+  grid_dep_wait();
+  grid_dep_trigger();
+  const int slices = P.DV / COLS;
+  const int unit = blockIdx.x / slices, c0 = COLS * (blockIdx.x % slices);
+  const int b = unit / P.HV, h = unit % P.HV, hk = h / (P.HV / P.HK);
+  const int c = threadIdx.x % LN, r = threadIdx.x / LN;
+  int row, begin, end;
+  if (blockIdx.x == 0 && P.items) {
+    // for the launch behind this one, most of whose blocks may have nothing to do
+    __shared__ unsigned long long items;
+    if (threadIdx.x == 0) items = 0;
+    __syncthreads();
+    unsigned long long mine = 0;
+    for (int j = threadIdx.x; j < P.B; j += DD_THREADS) {
+      begin = P.cu[j], end = P.cu[j + 1];
+      if (begin >= 0 && end <= P.T && end - begin > P.few) mine += (end - begin + P.L - 1) / P.L;
+    }
+    if (mine) atomicAdd(&items, mine);
+    __syncthreads();
+    if (threadIdx.x == 0) *P.items = (int)min(items, 0x7FFFFFFFull);
+  }
+  if (!sequence_rows(P, b, row, begin, end)) return;  // holds the block's barrier
+  if (begin == end || end - begin > P.few) return;
+  auto fetch = [&](int t0, int to) {
+    constexpr int QU = DK / 8, UNITS = 2 * QU + COLS / 8;  // of 16 bytes
+    const int m = min(DF_TOKENS, end - t0);
+    for (int i = threadIdx.x; i < m * UNITS; i += DD_THREADS) {
+      const int u = i / UNITS, x = i % UNITS, t = t0 + u;
+      const uint16_t* from = x < QU       ? P.q + t * P.ldq + hk * DK + 8 * x
+                             : x < 2 * QU ? P.k + t * P.ldk + hk * DK + 8 * (x - QU)
+                                          : P.v + t * P.ldv + h * P.DV + c0 + 8 * (x - 2 * QU);
+      copy_async<16>(&raw[to][u][8 * x], from);
+    }
+    if (threadIdx.x < m)
+      copy_async<4>(&log_decay[to][threadIdx.x], P.g + (t0 + (int)threadIdx.x) * P.ldg + h);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  fetch(begin, 0);
+  float* S = P.state + (((size_t)row * P.HV + h) * DK + N * r) * P.DV + c0 + 4 * c;
+  f32x2 s[N][2];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(S + (size_t)i * P.DV);
+    s[i][0] = x.x, s[i][1] = x.y;
+  }
+  int at = 0;
+#pragma unroll 1
+  for (int t0 = begin; t0 < end; t0 += DF_TOKENS, at ^= 1) {
+    const int m = min(DF_TOKENS, end - t0);
+    if (t0 + DF_TOKENS < end) {
+      fetch(t0 + DF_TOKENS, at ^ 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < m * DK; i += DD_THREADS) {
+      const int u = i / DK, x = i % DK;
+      const float q = bf1(raw[at][u][x]), k = bf1(raw[at][u][DK + x]);
+      qs[u][x] = pair_of(q, q);
+      ks[u][x] = pair_of(k, k);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < DF_TOKENS; ++u) {
+      if (u >= m) break;
+      const uint2 vw = *reinterpret_cast<const uint2*>(&raw[at][u][2 * DK + 4 * c]);
+      const f32x2 v0 = pair_of(bf_lo(vw.x), bf_hi(vw.x)), v1 = pair_of(bf_lo(vw.y), bf_hi(vw.y));
+      const float e = expf(log_decay[at][u]);
+      const f32x2 a = pair_of(e, e);
+      f32x2 o0 = 0, o1 = 0;
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&ks[u][N * r + i]);
+        const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(&qs[u][N * r + i]);
+        s[i][0] = fma2(s[i][0], a, mul2(k.x, v0)), o0 = fma2(q.x, s[i][0], o0);
+        s[i][1] = fma2(s[i][1], a, mul2(k.x, v1)), o1 = fma2(q.x, s[i][1], o1);
+        s[i + 1][0] = fma2(s[i + 1][0], a, mul2(k.y, v0)), o0 = fma2(q.y, s[i + 1][0], o0);
+        s[i + 1][1] = fma2(s[i + 1][1], a, mul2(k.y, v1)), o1 = fma2(q.y, s[i + 1][1], o1);
+      }
+      const float2 lo = halves(o0), hi = halves(o1);
+      float4 o = make_float4(lo.x, lo.y, hi.x, hi.y);
+#pragma unroll
+      for (int x = LN; x < 32; x <<= 1) {
+        o.x += __shfl_xor_sync(0xffffffffu, o.x, x), o.y += __shfl_xor_sync(0xffffffffu, o.y, x);
+        o.z += __shfl_xor_sync(0xffffffffu, o.z, x), o.w += __shfl_xor_sync(0xffffffffu, o.w, x);
+      }
+      if ((threadIdx.x & 31) < LN) part[u][threadIdx.x >> 5][threadIdx.x & 31] = o;
+    }
+    __syncthreads();
+    if (threadIdx.x < m * LN) {
+      const int u = threadIdx.x / LN, x = threadIdx.x % LN;
+      float4 o = part[u][0][x];
+#pragma unroll
+      for (int w = 1; w < WARPS; ++w) {
+        const float4 y = part[u][w][x];
+        o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
+      }
+      *reinterpret_cast<uint2*>(P.o + (t0 + u) * P.ldo + h * P.DV + c0 + 4 * x) = make_uint2(
+          pack2_bf(P.scale * o.x, P.scale * o.y), pack2_bf(P.scale * o.z, P.scale * o.w));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    *reinterpret_cast<ulonglong2*>(S + (size_t)i * P.DV) = make_ulonglong2(s[i][0], s[i][1]);
+}
+
+int launch_few(const DecayParams& P, cudaStream_t st) {
+  // as for single tokens
+  const int units = P.B * P.HV;
+  const int cols = units >= 2 * num_sms() ? P.DV : 32;
+  const int blocks = units * (P.DV / cols);
+  if (P.DK == 64)
+    return launch_pdl(cols == 128  ? k_decay_few<64, 128>
+                      : cols == 64 ? k_decay_few<64, 64>
+                                   : k_decay_few<64, 32>,
+                      blocks, DD_THREADS, P, st);
+  return launch_pdl(cols == 128  ? k_decay_few<128, 128>
+                    : cols == 64 ? k_decay_few<128, 64>
+                                 : k_decay_few<128, 32>,
+                    blocks, DD_THREADS, P, st);
+}
+
 // ------------------------------------------------------------ prompts
 // A sequence is walked in chunks of 128 tokens.  With G_i the sum of the log-decays of
 // a chunk's tokens 0..i and S the state in front of it:
@@ -170,7 +352,8 @@ int launch_decode(const DecayParams& P, cudaStream_t st) {
 // 165, the join 10, the walk 340.  A walk's chunk takes about 4800 cycles: two
 // chains (Q Kᵀ - decayed - times V, and the state out of TMEM - Q S - Kᵀ Ṽ) that meet in
 // every chunk, each a row of waits of some hundred cycles, over 400 KB of shared-memory
-// traffic (3100 cycles); a chunk of STATES takes 2040, the latency of its decays' sums.
+// traffic (3100 cycles); a chunk of STATES takes 2040, as long as its decays' sums, its
+// terms and its loads each take for themselves.
 // The tensor cores are busy 16-25%.  Chunks of 64 tokens would have the same waits for half of
 // the tokens; slices of 128 columns have no room beside two chunks of k and v in shared
 // memory and three terms of the state in TMEM.
@@ -190,7 +373,6 @@ struct ChunkParams {
   CUtensorMap q_map, k_map, v_map;  // rows of [T][heads · dim], boxes 64 x 128
   CUtensorMap o_map;                // the same, boxes 32 x 32
   DecayParams d;
-  int L;        // tokens of a segment (a multiple of CH)
   float* W;     // [slots][HV][DK][DV] what a segment leaves, for sequences of two and more
   double* Wg;   // [slots][HV] a segment's log2 decay
 };
@@ -210,24 +392,29 @@ struct Item {
   int found, row, b, seg, nseg, slot, t0, t1;
 };
 
-// Segment `index` of the call's sequences, or the first one of sequence `index`, by one
-// warp; reports bad rows.
-template <bool SEQUENCE>
-__device__ __forceinline__ void find_item(const DecayParams& P, int L, int index, Item* out) {
+// Segment `index` of the sequences that have LEAST segments and more (LEAST 3: the first one
+// of sequence `index` of these), by one warp; reports bad rows.
+template <int LEAST>
+__device__ __forceinline__ void find_item(const DecayParams& P, int index, Item* out) {
   const int lane = threadIdx.x & 31;
   int acc = 0, slots = 0;
   long long tokens = 0;
   Item it{};
+  int next[3];
+  auto fetch = [&](int b) {
+    next[0] = b < P.B ? P.cu[b] : 0;
+    next[1] = b < P.B ? P.cu[b + 1] : 0;
+    next[2] = b < P.B ? P.seq_ids[b] : 0;
+  };
+  fetch(lane);
 #pragma unroll 1
   for (int b0 = 0; b0 < P.B; b0 += 32) {
-    const int b = b0 + lane;
-    int n = 0, begin = 0, end = 0, row = 0;
-    if (b < P.B) {
-      begin = P.cu[b], end = P.cu[b + 1], row = P.seq_ids[b];
-      if (begin < 0 || end < begin || end > P.T || row < 0 || row >= P.s_max) {
-        set_dev_error(P.err, ER_EINVAL);
-        end = begin;
-      }
+    const int b = b0 + lane, begin = next[0], row = next[2];
+    int end = next[1];
+    fetch(b + 32);
+    if (begin < 0 || end < begin || end > P.T || row < 0 || row >= P.s_max) {
+      set_dev_error(P.err, ER_EINVAL);
+      end = begin;
     }
     // together they have T tokens at most: the segments that the grid and the workspace
     // have room for
@@ -238,18 +425,19 @@ __device__ __forceinline__ void find_item(const DecayParams& P, int L, int index
       if (lane >= m) len += x - tokens;
     }
     tokens = __shfl_sync(0xffffffffu, len, 31);
+    int segs = 0;
     if (len <= P.T)
-      n = (end - begin + L - 1) / L;
+      segs = end - begin > P.few ? (end - begin + P.L - 1) / P.L : 0;
     else if (end > begin)
       set_dev_error(P.err, ER_EINVAL);
-    int sum = n, many = n > 1 ? n : 0;
+    const int n = segs < LEAST ? 0 : LEAST == 3 ? 1 : segs;
+    int sum = n, many = segs > 1 ? segs : 0;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, sum, m), y = __shfl_up_sync(0xffffffffu, many, m);
       if (lane >= m) sum += x, many += y;
     }
-    const unsigned hit =
-        __ballot_sync(0xffffffffu, SEQUENCE ? b == index && n > 0 : acc + sum > index);
+    const unsigned hit = __ballot_sync(0xffffffffu, acc + sum > index);
     if (hit) {
       const int l = __ffs(hit) - 1;
       // an earlier sequence with the same state row?
@@ -261,11 +449,11 @@ __device__ __forceinline__ void find_item(const DecayParams& P, int L, int index
         return;
       }
       if (lane == l) {
-        it.found = 1, it.row = row, it.b = b, it.nseg = n;
-        it.seg = SEQUENCE ? 0 : index - (acc + sum - n);
-        it.slot = slots + many - (n > 1 ? n : 0);
-        it.t0 = begin + L * it.seg;
-        it.t1 = min(end, it.t0 + L);
+        it.found = 1, it.row = row, it.b = b, it.nseg = segs;
+        it.seg = LEAST == 3 ? 0 : index - (acc + sum - n);
+        it.slot = slots + many - (segs > 1 ? segs : 0);
+        it.t0 = begin + P.L * it.seg;
+        it.t1 = min(end, it.t0 + P.L);
         *out = it;
       }
       return;
@@ -381,7 +569,8 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   }
   grid_dep_wait();
   grid_dep_trigger();
-  if (warp == 0) find_item<false>(D, P.L, blockIdx.x / per, &B.item);
+  if (D.items && (int)(blockIdx.x / per) >= *D.items) return;
+  if (warp == 0) find_item<STATES ? 2 : 1>(D, blockIdx.x / per, &B.item);
   if (threadIdx.x == 32) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&B.k_full[i], 1);
@@ -412,7 +601,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   }
   __syncthreads();
   const Item it = B.item;
-  if (!it.found || (STATES && it.nseg < 2)) return;
+  if (!it.found) return;
   const size_t plane = (size_t)DK * D.DV;
   float* W0 = P.W + ((size_t)it.slot * D.HV + h) * plane;
   if (STATES && it.seg == it.nseg - 1) {
@@ -931,10 +1120,10 @@ __global__ void __launch_bounds__(DJ_THREADS) k_decay_join(const ChunkParams P) 
   grid_dep_wait();
   grid_dep_trigger();
   const int plane = D.DK * D.DV, parts = plane / (4 * DJ_THREADS), per = D.HV * parts;
-  if (threadIdx.x < 32) find_item<true>(D, P.L, blockIdx.x / per, &item);
+  if (threadIdx.x < 32) find_item<3>(D, blockIdx.x / per, &item);
   __syncthreads();
   const Item it = item;
-  if (!it.found || it.nseg < 3) return;
+  if (!it.found) return;
   const int h = blockIdx.x % per / parts, part = blockIdx.x % parts;
   const size_t step = (size_t)D.HV * plane;
   float* W = P.W + it.slot * step + (size_t)h * plane + 4 * (part * DJ_THREADS + threadIdx.x);
@@ -979,19 +1168,42 @@ int segment_tokens(int T, int HV, int DV) {
 // ceil(n / L) < 2 n / L.
 size_t segment_slots(int T, int L) { return T > L ? 2 * (size_t)T / L : 0; }
 
-size_t prefill_bytes(int T, int HV, int DK, int DV, float** W, double** Wg, void* base) {
+size_t prefill_bytes(int T, int HV, int DK, int DV, float** W, double** Wg, int32_t** items,
+                     void* base) {
   const size_t slots = segment_slots(T, segment_tokens(T, HV, DV));
   Carver c(base);
   float* w = c.take<float>(slots * HV * DK * DV);
   double* g = c.take<double>(slots * HV + 1);
-  if (W) *W = w, *Wg = g;
+  int32_t* n = c.take<int32_t>(1);
+  if (W) *W = w, *Wg = g, *items = n;
   return c.used();
 }
 
 std::mutex g_attr_mu;
 bool g_attr_done[64] = {false};
 
-int launch_prefill(const DecayParams& D, void* ws, cudaStream_t st) {
+// Sequences of how many tokens k_decay_few takes.
+int few_tokens(const DecayParams& D) {
+  // Where heads fill the SMs, up to 32: 16 sequences of 16 tokens take 34 us (by chunks 57),
+  // of 32 59 (57), of 60 106 (65); 512 of 32 1640 us (above 2200).  Else, with narrower slices, 16:
+  // one of 8 tokens takes 4.3 us, of 16 6.6 (8.2).
+  const int most = D.B * D.HV >= 2 * num_sms() ? 32 : 16;
+  // its launch for nothing costs 2 us: only where the mean length is below a chunk's
+  return D.T <= most || D.T < (int64_t)CH * D.B ? most : 0;
+}
+
+int launch_prefill(DecayParams D, void* ws, cudaStream_t st) {
+  ChunkParams P{};
+  int32_t* items;
+  prefill_bytes(D.T, D.HV, D.DK, D.DV, &P.W, &P.Wg, &items, ws);
+  D.L = segment_tokens(D.T, D.HV, D.DV);
+  D.few = few_tokens(D);
+  if (D.few) {
+    D.items = items;
+    const int rc = launch_few(D, st);
+    if (rc != ER_OK || D.T <= D.few) return rc;
+  }
+  P.d = D;
   {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return ER_ECUDA;
@@ -1006,10 +1218,6 @@ int launch_prefill(const DecayParams& D, void* ws, cudaStream_t st) {
       g_attr_done[dev] = true;
     }
   }
-  ChunkParams P{};
-  P.d = D;
-  P.L = segment_tokens(D.T, D.HV, D.DV);
-  prefill_bytes(D.T, D.HV, D.DK, D.DV, &P.W, &P.Wg, ws);
   if (!encode_rows(&P.q_map, D.q, false, D.HK * D.DK, D.T, D.ldq * 2, 64, CH) ||
       !encode_rows(&P.k_map, D.k, false, D.HK * D.DK, D.T, D.ldk * 2, 64, CH) ||
       !encode_rows(&P.v_map, D.v, false, D.HV * D.DV, D.T, D.ldv * 2, 64, CH) ||
@@ -1019,29 +1227,36 @@ int launch_prefill(const DecayParams& D, void* ws, cudaStream_t st) {
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  const size_t segs = (size_t)D.B + (D.T > P.L ? D.T / P.L : 0);
-  const size_t blocks = segs * D.HV * (D.DV / 64);
-  const size_t parts = (size_t)D.B * D.HV * (D.DK * D.DV / (4 * DJ_THREADS));  // of the second launch
-  if (blocks > 0x7FFFFFFFu || parts > 0x7FFFFFFFu) return ER_EINVAL;
-  cfg.gridDim = dim3((unsigned)blocks);
+  // sequences of more than n tokens are T / (n + 1) at most, and the segments of m sequences
+  // m + T / L
+  const auto sequences = [&](size_t n) { return std::min((size_t)D.B, D.T / (n + 1)); };
+  const size_t per = D.HV * (D.DV / 64), cut = D.T > D.L ? D.T / D.L : 0;
+  const size_t blocks = (sequences(D.few) + cut) * per;
+  const size_t first = (sequences(D.L) + cut) * per;
+  const size_t joins = sequences(2 * (size_t)D.L) * D.HV * (D.DK * D.DV / (4 * DJ_THREADS));
+  if (blocks > 0x7FFFFFFFu || joins > 0x7FFFFFFFu) return ER_EINVAL;
   cfg.blockDim = dim3(DC_THREADS);
   cfg.dynamicSmemBytes = chunk_smem(D.DK);
   cfg.stream = st;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
   const bool wide = D.DK == 128;
-  if (D.T > P.L) {
+  if (D.T > D.L) {
+    cfg.gridDim = dim3((unsigned)first);
     if (cudaLaunchKernelEx(&cfg, wide ? k_decay_chunks<128, true> : k_decay_chunks<64, true>, P) !=
         cudaSuccess)
       return ER_ECUDA;
     count_launches(1);
+  }
+  if (joins) {
     cudaLaunchConfig_t join = cfg;
-    join.gridDim = dim3((unsigned)parts);
+    join.gridDim = dim3((unsigned)joins);
     join.blockDim = dim3(DJ_THREADS);
     join.dynamicSmemBytes = 0;
     if (cudaLaunchKernelEx(&join, k_decay_join, P) != cudaSuccess) return ER_ECUDA;
     count_launches(1);
   }
+  cfg.gridDim = dim3((unsigned)blocks);
   if (cudaLaunchKernelEx(&cfg, wide ? k_decay_chunks<128, false> : k_decay_chunks<64, false>, P) !=
       cudaSuccess)
     return ER_ECUDA;
@@ -1092,7 +1307,8 @@ extern "C" {
 
 size_t er_decay_prefill_workspace_bytes(const er_decay_shape* shape, int32_t B, int32_t T) {
   if (!shape_ok(shape) || B < 1 || B > 65535 || T < 0 || T > (1 << 30)) return 0;
-  return prefill_bytes(T, shape->v_heads, shape->k_dim, shape->v_dim, nullptr, nullptr, nullptr);
+  return prefill_bytes(T, shape->v_heads, shape->k_dim, shape->v_dim, nullptr, nullptr, nullptr,
+                       nullptr);
 }
 
 int er_decay_decode(float* state, int32_t s_max, const int32_t* seq_ids, int32_t B,

@@ -130,6 +130,46 @@ def test_prefill(sab, lengths, HK, HV, DK, DV):
     assert torch.equal(again, S) and torch.equal(out, out2)
 
 
+@pytest.mark.parametrize("HK,HV,DK,DV", HEADS)
+@pytest.mark.parametrize("lengths", [
+    [3], [16], [17], [4] * 3, [16] * 40, [2, 0, 7, 16, 1, 5, 0, 13], [1] * 300, [0] * 40 + [9],
+    [1] * 50 + [700], [17, 16, 15] * 12, [30] * 9, [600] + [3] * 70])
+def test_short_sequences(sab, lengths, HK, HV, DK, DV):
+    """Sequences of few tokens, alone and among longer ones.  Where all have 16 at most, each
+    step costs an exponential (2^-22) and a rounding (2^-24) of A: together 2^-17 at most."""
+    decay = "head" if len(lengths) % 3 == 0 else "token"
+    c = Case(lengths, HK, HV, DK, DV, rows=len(lengths) + 2, decay=decay)
+    S = c.state.clone()
+    o = sab.decay_prefill(S, c.ids, c.cu, c.q, c.k, c.v, c.g)
+    assert sab.last_call_error() == 0
+    c.check(o, S)
+    if max(lengths) <= 16:
+        _, _, want, A = c.want()
+        assert bool(((S.double() - want).abs() <= 2.0 ** -17 * A + 1e-30).all())
+    unused = [r for r in range(c.B + 2) if r not in c.ids.tolist()]
+    unused += [int(c.ids[b]) for b in range(c.B) if lengths[b] == 0]
+    assert torch.equal(S[unused], c.state[unused])
+    again = c.state.clone()
+    assert torch.equal(sab.decay_prefill(again, c.ids, c.cu, c.q, c.k, c.v, c.g), o)
+    assert torch.equal(again, S)
+
+
+@pytest.mark.parametrize("lengths", [[3, 4, 5, 2], [3, 200, 5, 20]])
+def test_short_sequences_with_bad_rows(sab, lengths):
+    c = Case(lengths, 2, 4, 64, 64, rows=6)
+    for at, bad in ((2, -1), (2, 6), (2, int(c.ids[0])), (3, int(c.ids[1]))):
+        ids = c.ids.clone()
+        ids[at] = bad
+        S, out = c.state.clone(), torch.full((c.T, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        sab.decay_prefill(S, ids, c.cu, c.q, c.k, c.v, c.g, out=out)
+        assert sab.last_call_error() == -1 and sab.last_call_error() == 0
+        d = Case(lengths, 2, 4, 64, 64, rows=6)
+        d.lengths[at] = 0
+        there = d.check(out, S)
+        assert bool((out[~there] == 7).all())
+        assert int((~there).all(2).all(1).sum()) == lengths[at]
+
+
 @pytest.mark.parametrize("HK,HV,DK,DV,n", [(1, 1, 128, 128, 9000), (1, 2, 64, 64, 20011),
                                            (2, 2, 64, 128, 4097), (1, 1, 128, 64, 6300)])
 def test_long_prompts(sab, HK, HV, DK, DV, n):
