@@ -1155,22 +1155,47 @@ constexpr int chunk_smem(int DK) {
   return 512 * DK + (walk > states ? walk : states) + 10240;
 }
 
-// Tokens of a segment: so many that the segments of one sequence of T tokens give
-// every SM about four walks, but 512 at least.
-int segment_tokens(int T, int HV, int DV) {
-  const int walks = HV * (DV / 64), want = 4 * num_sms() / walks;
-  if (want <= 1) return (T + CH - 1) / CH * CH;
-  const int L = ((T + want - 1) / want + CH - 1) / CH * CH;
-  return L < 512 ? 512 : L;
+// Tokens of a segment: the cut with the least estimated time, of cuts that fill 1 to 8 rounds
+// of the SMs, of none, and of one into the call's sequences.  The lengths are not known here: it
+// is the time if one sequence has all tokens, plus that if all have as many.  Measured: a
+// walk takes 5.5 us and 2.6 a chunk, one of the states' 2.5 and 1.1, their launch and the
+// join's 7 and 0.2 a segment.  (32 heads of 128 x 128, by this and with four rounds and 512
+// tokens at least: 1500 tokens 37 and 48 us, 4096 75 and 109, 8192 135 and 169, 32768 474 and 474;
+// 8 heads of 64 x 64, 32768 tokens 70 and 110.)
+int segment_tokens(int B, int T, int HV, int DV) {
+  const int walks = HV * (DV / 64), sms = num_sms();
+  const auto chunks = [](int tokens) { return std::max(1, (tokens + CH - 1) / CH); };
+  const auto cost = [&](int n, int all, int len) {  // n sequences of `all` chunks
+    const long long w = (long long)n * walks;
+    const auto rounds = [&](int segs) { return (double)((w * segs + sms - 1) / sms); };
+    const int segs = (all + len - 1) / len;
+    if (segs == 1) return rounds(1) * (5.5 + 2.6 * all);
+    return rounds(segs) * (5.5 + 2.6 * len) + 7.0 + 0.2 * segs +
+           rounds(segs - 1) * (2.5 + 1.1 * len);
+  };
+  const int one = chunks(T), each = chunks((T + B - 1) / B);
+  int best = one;
+  double least = 1e300;
+  const auto consider = [&](int len) {
+    const double t = cost(1, one, len) + cost(B, each, len);
+    if (t < least) least = t, best = len;
+  };
+  consider(one);
+  consider(each);
+  for (int r = 1; r <= 8; ++r) {
+    const int segs = std::min(one, r * sms / walks);
+    if (segs > 1) consider((one + segs - 1) / segs);
+  }
+  return CH * best;
 }
 
 // Segments of sequences that have two and more: a sequence of n > L tokens has
 // ceil(n / L) < 2 n / L.
 size_t segment_slots(int T, int L) { return T > L ? 2 * (size_t)T / L : 0; }
 
-size_t prefill_bytes(int T, int HV, int DK, int DV, float** W, double** Wg, int32_t** items,
+size_t prefill_bytes(int B, int T, int HV, int DK, int DV, float** W, double** Wg, int32_t** items,
                      void* base) {
-  const size_t slots = segment_slots(T, segment_tokens(T, HV, DV));
+  const size_t slots = segment_slots(T, segment_tokens(B, T, HV, DV));
   Carver c(base);
   float* w = c.take<float>(slots * HV * DK * DV);
   double* g = c.take<double>(slots * HV + 1);
@@ -1195,8 +1220,8 @@ int few_tokens(const DecayParams& D) {
 int launch_prefill(DecayParams D, void* ws, cudaStream_t st) {
   ChunkParams P{};
   int32_t* items;
-  prefill_bytes(D.T, D.HV, D.DK, D.DV, &P.W, &P.Wg, &items, ws);
-  D.L = segment_tokens(D.T, D.HV, D.DV);
+  prefill_bytes(D.B, D.T, D.HV, D.DK, D.DV, &P.W, &P.Wg, &items, ws);
+  D.L = segment_tokens(D.B, D.T, D.HV, D.DV);
   D.few = few_tokens(D);
   if (D.few) {
     D.items = items;
@@ -1307,7 +1332,7 @@ extern "C" {
 
 size_t er_decay_prefill_workspace_bytes(const er_decay_shape* shape, int32_t B, int32_t T) {
   if (!shape_ok(shape) || B < 1 || B > 65535 || T < 0 || T > (1 << 30)) return 0;
-  return prefill_bytes(T, shape->v_heads, shape->k_dim, shape->v_dim, nullptr, nullptr, nullptr,
+  return prefill_bytes(B, T, shape->v_heads, shape->k_dim, shape->v_dim, nullptr, nullptr, nullptr,
                        nullptr);
 }
 
