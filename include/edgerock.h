@@ -349,8 +349,8 @@ int er_gated_linear(const er_bf16* x, int32_t ldx, int32_t T, const er_bf16* w_g
  *  A sequence whose state row is out of range or was listed before it in the
  *  call, or whose rows leave [0, T), is skipped (its state and its rows of o are
  *  left as they are) and records ER_EINVAL in *dev_error (NULL: the library's own
- *  word, er_last_call_error); so are sequences past the first T tokens of a
- *  call.  The same inputs give the same bits. */
+ *  word, er_last_call_error); so may be sequences whose rows belong to others too.
+ *  The same inputs give the same bits. */
 typedef struct er_decay_shape {
   int32_t k_heads, v_heads, k_dim, v_dim;
 } er_decay_shape;

@@ -348,8 +348,8 @@ int launch_few(const DecayParams& P, cudaStream_t st) {
 // segment's chunks are walked from its end, so that all decays are known and no
 // product waits for another.
 //
-// What bounds it: 32768 tokens of 32 heads of 128 x 128 (16 of q and k) take 535 us: STATES
-// 165, the join 10, the walk 340.  A walk's chunk takes about 4800 cycles: two
+// What bounds it: 32768 tokens of 32 heads of 128 x 128 (16 of q and k) take 475 us, of these
+// STATES 0.31, the join 0.02 and the walk 0.67.  A walk's chunk takes about 4800 cycles: two
 // chains (Q Kᵀ - decayed - times V, and the state out of TMEM - Q S - Kᵀ Ṽ) that meet in
 // every chunk, each a row of waits of some hundred cycles, over 400 KB of shared-memory
 // traffic (3100 cycles); a chunk of STATES takes 2040, as long as its decays' sums, its
