@@ -297,19 +297,26 @@ def _wrong(t, device, dtype, shape, name):
 
 
 def _arg(t, device, dtype, shape, name):
-    """The address of a tensor whose last dimensions are dense and whose rows
-    (dimension 0) may be strided, and that row stride in elements."""
+    """The address of a tensor of two or three dimensions whose last ones are dense and whose
+    rows (dimension 0) may be strided, and that row stride in elements."""
     if t.shape != shape or t.dtype != dtype or t.device != device:
         _wrong(t, device, dtype, shape, name)
     st = t.stride()
-    dense = 1
-    for i in range(len(shape) - 1, 0, -1):
-        if st[i] != dense and shape[i] != 1:
-            raise ValueError(f"{name} must have dense rows, got strides {st}")
-        dense *= shape[i]
+    if len(shape) == 2:
+        rows, dense = shape
+        ld, inner = st
+        fine = inner == 1 or dense == 1
+    else:
+        rows, heads, width = shape
+        ld, outer, inner = st
+        dense = heads * width
+        fine = (inner == 1 or width == 1) and (outer == width or heads == 1)
+    if not fine:
+        raise ValueError(f"{name} must have dense rows, got strides {st}")
     # a single row's stride says nothing
-    ld = st[0] if shape[0] > 1 else dense
-    if ld < dense:
+    if rows <= 1:
+        ld = dense
+    elif ld < dense:
         raise ValueError(f"{name} must not have overlapping rows, got strides {st}")
     return t.data_ptr(), ld
 
@@ -387,34 +394,45 @@ def _index(t, device, name):
     return t
 
 
-def _decay_shape(state, q, v):
-    if state.dim() != 4 or q.dim() != 3 or v.dim() != 3:
+_shape_of = functools.lru_cache(maxsize=256)(_lib.CDecayShape)
+
+
+def _decay_state(state, device, q):
+    """The state's address, its rows, and the call's shape as numbers and as a struct."""
+    if state.dim() != 4 or q.dim() != 3:
         raise ValueError("state must be [rows, v_heads, k_dim, v_dim], q, k [T, k_heads, k_dim], "
                          "v [T, v_heads, v_dim]")
-    return _lib.CDecayShape(q.shape[1], *state.shape[1:])
+    rows, HV, DK, DV = state.shape
+    HK = q.shape[1]
+    if state.dtype != torch.float32 or not state.is_contiguous():
+        _dense(state, device, torch.float32, state.shape, "state")
+    return state.data_ptr(), rows, (HK, HV, DK, DV), _shape_of(HK, HV, DK, DV)
 
 
-def _decay_rows(device, sh, T, q, k, v, log_decay, scale, out):
+def _decay_rows(device, heads, T, q, k, v, log_decay, scale, out):
     """The arguments q .. o of the decay calls, and out."""
     bf = torch.bfloat16
-    qk, vo = (T, sh.k_heads, sh.k_dim), (T, sh.v_heads, sh.v_dim)
+    HK, HV, DK, DV = heads
+    qk, vo = (T, HK, DK), (T, HV, DV)
     if out is None:
         out = torch.empty(vo, dtype=bf, device=device)
-    if log_decay.dim() == 2 and T > 1 and log_decay.stride(0) == 0:
+    per_token = log_decay.dim() == 2
+    if per_token and T > 1 and log_decay.stride(0) == 0:
         if log_decay.shape[0] != T:
             raise ValueError(f"log_decay must have {T} rows, got {log_decay.shape[0]}")
-        log_decay = log_decay[0]  # one row, expanded
-    if log_decay.dim() == 1:
-        pg, ldg = _dense(log_decay, device, torch.float32, (sh.v_heads,), "log_decay"), 0
+        log_decay, per_token = log_decay[0], False  # one row, expanded
+    if per_token:
+        pg, ldg = _arg(log_decay, device, torch.float32, (T, HV), "log_decay")
     else:
-        pg, ldg = _arg(log_decay, device, torch.float32, (T, sh.v_heads), "log_decay")
+        pg, ldg = _dense(log_decay, device, torch.float32, (HV,), "log_decay"), 0
     return (*_arg(q, device, bf, qk, "q"), *_arg(k, device, bf, qk, "k"),
             *_arg(v, device, bf, vo, "v"), pg, ldg,
-            sh.k_dim ** -0.5 if scale is None else scale, *_arg(out, device, bf, vo, "out")), out
+            DK ** -0.5 if scale is None else scale, *_arg(out, device, bf, vo, "out")), out
 
 
 @_on_stream
-def decay_decode(state: torch.Tensor, seq_ids, q, k, v, log_decay, scale=None, out=None, dev_error=None):
+def decay_decode(state: torch.Tensor, seq_ids, q, k, v, log_decay, scale=None, out=None,
+                 dev_error=None):
     """One token for each of B sequences through linear attention with a decay for each head
     (er_decay_decode): S = e^g S + k vᵀ, o = scale · Sᵀ q.  state FP32 [rows, v_heads, k_dim,
     v_dim], rows seq_ids updated in place; q, k BF16 [B, k_heads, k_dim], v BF16 [B, v_heads,
@@ -423,11 +441,10 @@ def decay_decode(state: torch.Tensor, seq_ids, q, k, v, log_decay, scale=None, o
     device = _device_of(state, "state")
     ids = _index(seq_ids, device, "seq_ids")
     B = ids.numel()
-    sh = _decay_shape(state, q, v)
-    rows, out = _decay_rows(device, sh, B, q, k, v, log_decay, scale, out)
-    _call("er_decay_decode", device,
-          _dense(state, device, torch.float32, state.shape, "state"), state.shape[0],
-          ids.data_ptr(), B, sh, *rows, _error_word(dev_error, device))
+    ps, s_max, heads, sh = _decay_state(state, device, q)
+    rows, out = _decay_rows(device, heads, B, q, k, v, log_decay, scale, out)
+    _call("er_decay_decode", device, ps, s_max, ids.data_ptr(), B, sh, *rows,
+          _error_word(dev_error, device))
     return out
 
 
@@ -447,19 +464,18 @@ def decay_prefill(state: torch.Tensor, seq_ids, cu_tokens, q, k, v, log_decay, s
     equals token by token."""
     device = _device_of(state, "state")
     ids, cu = _index(seq_ids, device, "seq_ids"), _index(cu_tokens, device, "cu_tokens")
-    B, T = ids.numel(), q.shape[0]
+    B = ids.numel()
     if cu.numel() != B + 1:
         raise ValueError(f"cu_tokens must have {B + 1} entries, got {cu.numel()}")
-    sh = _decay_shape(state, q, v)
-    rows, out = _decay_rows(device, sh, T, q, k, v, log_decay, scale, out)
-    nb = decay_prefill_workspace_bytes(sh.k_heads, sh.v_heads, sh.k_dim, sh.v_dim, B, T) if B else 0
+    ps, s_max, heads, sh = _decay_state(state, device, q)
+    T = q.shape[0]
+    rows, out = _decay_rows(device, heads, T, q, k, v, log_decay, scale, out)
+    nb = decay_prefill_workspace_bytes(*heads, B, T) if B else 0
     if ws is not None and ws.device != device:
         raise ValueError(f"ws must be on {device}, got {ws.device}")
     ws = _ws(nb, device, ws)
-    _call("er_decay_prefill", device,
-          _dense(state, device, torch.float32, state.shape, "state"), state.shape[0],
-          ids.data_ptr(), cu.data_ptr(), B, T, sh, *rows, ws.data_ptr(), ws.numel(),
-          _error_word(dev_error, device))
+    _call("er_decay_prefill", device, ps, s_max, ids.data_ptr(), cu.data_ptr(), B, T, sh, *rows,
+          ws.data_ptr(), ws.numel(), _error_word(dev_error, device))
     return out
 
 
