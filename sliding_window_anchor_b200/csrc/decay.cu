@@ -156,10 +156,10 @@ int launch_decode(const DecayParams& P, cudaStream_t st) {
 // the state is read and written once, whatever their number.  A thread's rows follow one
 // another; k and q of four tokens are in shared memory as pairs of equal values, for
 // products on pairs of columns (fma.f32x2), while the next four tokens' rows are on their
-// way.  HBM bounds it for few tokens (512 sequences of 4, 32 heads of 128 x 128: 480 us, of
-// 1: 350), the FP32 products from about 8 on (of 16: 970): three for each value of the state
-// and token.  Eight columns a thread, with half of the fetches from shared memory, took
-// longer (550 and 1130 us).
+// way.  HBM bounds it for single tokens (512 sequences, 32 heads of 128 x 128: 350 us), then
+// more and more the tokens' own time, one after another in the two blocks that an SM holds:
+// 512 of 4 take 490 us, of 16 1000.  Eight columns a thread, with half of the fetches from
+// shared memory, took longer (550 and 1130 us).
 constexpr int DF_TOKENS = 4;  // between two barriers
 
 using f32x2 = unsigned long long;
