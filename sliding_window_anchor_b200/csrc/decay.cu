@@ -829,10 +829,8 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         uint32_t r[32], o[16];
         tc::tmem_ld32(tmem + lanes + T_P + y, r);
         tc::tmem_wait_ld();
-        // a column right of the diagonal is masked, whatever it holds
         const float row = g.row[i];
         const float* col = &g.col[col_at(quad) + y];
-        const int last = i - y;
 #pragma unroll
         for (int x = 0; x < 32; x += 4) {
           const float4 f = *reinterpret_cast<const float4*>(col + x);
@@ -840,8 +838,14 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
           const float p1 = __uint_as_float(r[x + 1]) * ex2(row + f.y);
           const float p2 = __uint_as_float(r[x + 2]) * ex2(row + f.z);
           const float p3 = __uint_as_float(r[x + 3]) * ex2(row + f.w);
-          o[x / 2] = pack2_bf(x <= last ? p0 : 0.f, x + 1 <= last ? p1 : 0.f);
-          o[x / 2 + 1] = pack2_bf(x + 2 <= last ? p2 : 0.f, x + 3 <= last ? p3 : 0.f);
+          o[x / 2] = pack2_bf(p0, p1);
+          o[x / 2 + 1] = pack2_bf(p2, p3);
+        }
+        if (cb == quad) {
+          // a column right of the diagonal is masked, whatever it holds
+#pragma unroll
+          for (int m = 0; m < 16; ++m)
+            o[m] &= 2 * m + 1 <= lane ? 0xFFFFFFFFu : 2 * m == lane ? 0xFFFFu : 0u;
         }
         tc::tmem_st16(tmem + lanes + T_P + y, o);
         if (cb == quad) {
