@@ -789,7 +789,9 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         const double x = __shfl_up_sync(0xffffffffu, sum, m);
         if (lane >= m) sum += x;
       }
-      const double front = sum - G[3], total = __shfl_sync(0xffffffffu, sum, 31);
+      // not sum - G[3]: a NaN of the lane's later tokens would reach its earlier ones
+      const double before = __shfl_up_sync(0xffffffffu, sum, 1);
+      const double front = lane ? before : 0.0, total = __shfl_sync(0xffffffffu, sum, 31);
       const double first = front + G[0], own = __shfl_sync(0xffffffffu, first, lane & ~7);
       double later[4];  // G at the blocks' first rows
 #pragma unroll
