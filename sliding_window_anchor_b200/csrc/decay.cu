@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "rounds.cuh"
 #include "tc.cuh"
 
 namespace er {
@@ -870,15 +871,17 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     const uint32_t sign = D.scale < 0.f ? 0x80008000u : 0u;
     float e = 0.f;
     int vs = 0, vp = 0;  // v's slot and phase
+    const auto meet = [] { named_bar_sync(1, 256); };
+    int c = 0;
 #pragma unroll 1
-    for (int c = 0; c <= n; ++c) {
+    for (; c <= n; ++c) {
       const float e_prev = e;
       if (c < n) {
         const int s = c & 1, t = it.t0 + CH * (STATES ? n - 1 - c : c) + j;
         if (!STATES) {
           if (tid < 64) B.colbad[c & 3][tid] = CH;
           if (tid == 64) B.anybad[c & 3] = 0;
-          named_bar_sync(1, 256);
+          meet();
         }
         if (!wait(&B.v_full[vs], vp) || !wait(&B.gate_full[s], c >> 1)) break;
         const float w = B.gate[s].w[j];
@@ -931,7 +934,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       }
       if (!STATES && c > 0) {
         const int cc = c - 1, t = it.t0 + CH * cc + j;
-        if (c == n) named_bar_sync(1, 256);  // the last chunk's marks
+        if (c == n) meet();  // the last chunk's marks
         if (!wait(&B.o_full, cc)) break;
         tc::fence_after_sync();
         const int col = 32 * half;
@@ -990,6 +993,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         }
       }
     }
+    if (!STATES) meet_rest(c, n, meet);
     if (!STATES && lane == 0) tc::bulk_wait_all();
   } else {
     // ------------------------------------------------------- the state
