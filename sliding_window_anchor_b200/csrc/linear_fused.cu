@@ -34,12 +34,29 @@ __device__ __forceinline__ float times_sigmoid(float v, float z) {
   return __fdividef(v, 1.f + __expf(-z));
 }
 
+// v · Φ(v).  The normal distribution's upper tail at x = |v| is t·P(t)·e^(-x²/2), t =
+// 1 / (1 + 0.305 x), the form of Abramowitz & Stegun 26.2.17; P is fitted for the least relative
+// error (2^-23.3) over x <= 13.2, behind which the tail is below the normal numbers.  No difference
+// of near values for v < 0, where v/2 · (1 + erf(v / sqrt(2))) is off by 4% at -5 and 0 from
+// -5.6 on.  Within (16 + 0.75 v²)·2^-23 of the value.  It takes as long as erff would;
+// v/2 · erfcf(-v / sqrt(2)) is as near and took a tenth longer (gated 300 x 2*9000 x 2560 36.3
+// against 32.8 us).
+__device__ __forceinline__ float gelu(float v) {
+  const float x = fabsf(v), t = __fdividef(1.f, fmaf(0.305f, x, 1.f));
+  float p = 0.0366991982f;
+  p = fmaf(p, t, -0.15298833f), p = fmaf(p, t, 0.185716912f), p = fmaf(p, t, -0.0379768424f);
+  p = fmaf(p, t, 0.121021688f), p = fmaf(p, t, 0.103420869f), p = fmaf(p, t, 0.122466817f);
+  p = fmaf(p, t, 0.121639736f);
+  const float tail = t * p * exp2f(-0.72134752044448170f * (x * x));
+  return v * (v < 0.f ? tail : 1.f - tail);
+}
+
 __device__ __forceinline__ float activate(float v, int act) {
   switch (act) {
     case ER_ACT_SILU:
       return times_sigmoid(v, v);
     case ER_ACT_GELU:
-      return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
+      return gelu(v);
     case ER_ACT_GELU_TANH:
       // 1 + tanh(z) = 2 / (1 + e^-2z)
       return times_sigmoid(v, 1.5957691216057308f * (v + 0.044715f * v * v * v));
