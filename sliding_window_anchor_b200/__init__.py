@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 
 import torch
 
@@ -244,15 +245,24 @@ def linear(x: torch.Tensor, w: torch.Tensor, fp32_out: bool = False, out=None, w
 
 def _on_stream(f):
     """`stream=`: run the call with that stream as the current one, so that what it
-    allocates belongs to the stream that uses it."""
+    allocates belongs to the stream that uses it.  The call's first argument is a tensor on
+    its device, by position or by name."""
+    sig = inspect.signature(f)
+    name = next(iter(sig.parameters))
+
     @functools.wraps(f)
-    def g(first, *args, stream=None, **kw):
-        if stream is None:
-            return f(first, *args, **kw)
-        if stream.device != first.device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {first.device}")
+    def g(*args, stream=None, **kw):
+        if stream is None or not (args or name in kw):
+            return f(*args, **kw)
+        device = (args[0] if args else kw[name]).device
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
         with torch.cuda.stream(stream):
-            return f(first, *args, **kw)
+            return f(*args, **kw)
+
+    g.__signature__ = sig.replace(parameters=[
+        *sig.parameters.values(),
+        inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY, default=None)])
     return g
 
 
