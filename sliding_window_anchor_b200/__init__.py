@@ -459,10 +459,20 @@ def decay_decode(state: torch.Tensor, seq_ids, q, k, v, log_decay, scale=None, o
 
 
 @functools.lru_cache(maxsize=256)
+def _prefill_bytes(index: int, heads, B: int, T: int) -> int:
+    """er_decay_prefill_workspace_bytes on device `index` (it depends on the number of SMs)."""
+    with torch.cuda.device(index):  # -1: no device, nothing to change
+        return int(lib().er_decay_prefill_workspace_bytes(_shape_of(*heads), B, T))
+
+
 def decay_prefill_workspace_bytes(k_heads: int, v_heads: int, k_dim: int, v_dim: int, B: int,
-                                  T: int) -> int:
-    return int(lib().er_decay_prefill_workspace_bytes(
-        _lib.CDecayShape(k_heads, v_heads, k_dim, v_dim), B, T))
+                                  T: int, device=None) -> int:
+    """The workspace of a decay_prefill call of these sizes on a device (default: the current
+    one)."""
+    index = None if device is None else torch.device(device).index
+    if index is None:
+        index = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    return _prefill_bytes(index, (k_heads, v_heads, k_dim, v_dim), B, T)
 
 
 @_on_stream
@@ -480,7 +490,7 @@ def decay_prefill(state: torch.Tensor, seq_ids, cu_tokens, q, k, v, log_decay, s
     ps, s_max, heads, sh = _decay_state(state, device, q)
     T = q.shape[0]
     rows, out = _decay_rows(device, heads, T, q, k, v, log_decay, scale, out)
-    nb = decay_prefill_workspace_bytes(*heads, B, T) if B else 0
+    nb = _prefill_bytes(device.index, heads, B, T) if B else 0
     if ws is not None and ws.device != device:
         raise ValueError(f"ws must be on {device}, got {ws.device}")
     ws = _ws(nb, device, ws)

@@ -1,5 +1,6 @@
-"""The binding of the fused products and the decayed attention on the host: arguments by name
-(CPU only)."""
+"""The binding of the fused products and the decayed attention on the host: arguments by name,
+workspaces by device (CPU only)."""
+import contextlib
 import inspect
 from types import SimpleNamespace
 
@@ -38,3 +39,41 @@ def test_signatures(name, args):
     shown = inspect.signature(getattr(sab, name)).parameters
     assert next(iter(shown)) == next(iter(args)) and set(args) <= set(shown)
     assert shown["stream"].default is None
+
+
+def test_workspace_size_is_that_of_the_tensors_device(monkeypatch):
+    """Devices of different SM counts need workspaces of different sizes for the same call."""
+    at = {"current": 0}
+
+    @contextlib.contextmanager
+    def device(index):
+        was, at["current"] = at["current"], index
+        yield
+        at["current"] = was
+
+    sizes = {0: 4096, 1: 8192}
+    fake = SimpleNamespace(
+        er_decay_prefill_workspace_bytes=lambda sh, B, T: sizes[at["current"]] + B + T)
+    monkeypatch.setattr(sab, "lib", lambda: fake)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: at["current"])
+    a = (16, 32, 128, 128, 2, 77773)
+    try:
+        for current in (0, 1, 0):
+            at["current"] = current
+            assert sab.decay_prefill_workspace_bytes(*a) == sizes[current] + 77775
+            for index in (1, 0):
+                assert sab.decay_prefill_workspace_bytes(*a, device=f"cuda:{index}") == \
+                    sizes[index] + 77775
+                assert sab._prefill_bytes(index, a[:4], *a[4:]) == sizes[index] + 77775
+            assert at["current"] == current
+    finally:
+        sab._prefill_bytes.cache_clear()
+
+
+def test_workspace_size_without_a_device():
+    if torch.cuda.is_available():
+        pytest.skip("there is a device")
+    assert sab.decay_prefill_workspace_bytes(2, 4, 64, 128, 4, 100) > 0
+    assert sab.decay_prefill_workspace_bytes(2, 4, 64, 100, 4, 100) == 0
