@@ -465,6 +465,16 @@ __device__ __forceinline__ void find_item(const DecayParams& P, int index, Item*
   if (lane == 0) *out = it;
 }
 
+// Reports sequence b when it is empty, so that no block has an item of it, and its state row
+// is listed before it; by one warp.
+__device__ __noinline__ void check_empty(const DecayParams& P, int b) {
+  if (b >= P.B || P.cu[b] != P.cu[b + 1]) return;
+  const int row = P.seq_ids[b];
+  bool same = false;
+  for (int j = threadIdx.x & 31; j < b; j += 32) same |= P.seq_ids[j] == row;
+  if (same) set_dev_error(P.err, ER_EINVAL);
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -572,6 +582,8 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   grid_dep_trigger();
   if (D.items && (int)(blockIdx.x / per) >= *D.items) return;
   if (warp == 0) find_item<STATES ? 2 : 1>(D, blockIdx.x / per, &B.item);
+  // where k_decay_few ran it has looked at every sequence; else there are B blocks at least
+  if (!STATES && warp == 2 && !D.items && blockIdx.x % per == 0) check_empty(D, blockIdx.x / per);
   if (threadIdx.x == 32) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&B.k_full[i], 1);
