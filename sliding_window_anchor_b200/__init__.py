@@ -444,7 +444,7 @@ def _decay_rows(device, heads, T, q, k, v, log_decay, scale, out):
 def decay_decode(state: torch.Tensor, seq_ids, q, k, v, log_decay, scale=None, out=None,
                  dev_error=None):
     """One token for each of B sequences through linear attention with a decay for each head
-    (er_decay_decode): S = e^g S + k vᵀ, o = scale · Sᵀ q.  state FP32 [rows, v_heads, k_dim,
+    (er_decay_decode; a general recurrence, not the delta rule): S = e^g S + k vᵀ, o = scale · Sᵀ q.  state FP32 [rows, v_heads, k_dim,
     v_dim], rows seq_ids updated in place; q, k BF16 [B, k_heads, k_dim], v BF16 [B, v_heads,
     v_dim] (rows may be strided: slices of one projection), log_decay FP32 [B, v_heads] or
     [v_heads]; scale defaults to k_dim ** -0.5; returns o BF16 [B, v_heads, v_dim]."""

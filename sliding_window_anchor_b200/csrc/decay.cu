@@ -1,12 +1,15 @@
-// decay.cu — linear attention with a decay for each head, for the recurrent
-// layers that stand between the SWA∥RMA layers of the model (EdgeRock-4B 开源：72 MiB
-// 固定 KV, §架构：递归、局部窗口与记忆锚点三件套: recurrent layers hold a matrix
-// of fixed size for each head, whatever the stream's length).
+// decay.cu — linear attention with a decay for each head: a recurrent layer whose state
+// is a matrix of fixed size for each head, whatever the stream's length.
 //
 //   S_t = e^{g_t} S_{t-1} + k_t v_tᵀ,   o_t = scale · S_tᵀ q_t
 //
 // per value head, S FP32 [k_dim][v_dim]; value head h reads the q and k of head
 // h / (v_heads / k_heads).
+//
+// A general operator for hybrid stacks.  The recurrent layers of the model whose SWA∥RMA
+// layers this library runs (EdgeRock-4B 开源：72 MiB 固定 KV, §架构：递归、局部窗口与
+// 记忆锚点三件套) hold such a state, too, but update it by the delta rule
+// (S ← (I - b k kᵀ) a S + b k vᵀ), which is not here.
 #include <algorithm>
 #include <mutex>
 
@@ -159,7 +162,7 @@ int launch_decode(const DecayParams& P, cudaStream_t st) {
 // products on pairs of columns (fma.f32x2), while the next four tokens' rows are on their
 // way.  HBM bounds it for single tokens (512 sequences, 32 heads of 128 x 128: 350 us), then
 // more and more the tokens' own time, one after another in the two blocks that an SM holds:
-// 512 of 4 take 490 us, of 16 1000.  Eight columns a thread, with half of the fetches from
+// 512 of 4 take 490-510 us, of 16 1000.  Eight columns a thread, with half of the fetches from
 // shared memory, took longer (550 and 1130 us).
 constexpr int DF_TOKENS = 4;  // between two barriers
 
@@ -335,12 +338,19 @@ int launch_few(const DecayParams& P, cudaStream_t st) {
 //   o_i = scale · (e^{G_i} Sᵀ q_i + Σ_{j<=i} (q_i·k_j) e^{G_i - G_j} v_j)
 //   S  <- e^{G_127} S + Σ_j k_j (e^{G_127 - G_j} v_j)ᵀ
 // as four tensor-core products (tcgen05): Q Kᵀ (masked and decayed in registers, back
-// into TMEM as BF16), that times V, Q S (S as BF16), Kᵀ Ṽ.  The state's product is
-// exact to 2^-24: its decayed values Ṽ go in as three BF16 terms; the state itself
-// stays in FP32 in TMEM, where the chunk's decay is applied to it.  Of
-// o's terms each meets one rounding to BF16 (2^-8), like its result.  G is summed in
-// FP64; differences go to FP32 relative to a row of the same 32 (with log-decays of -150
-// at least, they are off by 2^-12 at most).
+// into TMEM as BF16), that times V, Q S (S as BF16), Kᵀ Ṽ.  What is rounded:
+//  - the state's operand Ṽ goes in as three BF16 terms, which hold its FP32 values to
+//    2^-24; with one or two an error of 2^-8 or 2^-16 would be carried to every later token.
+//    The sums stay in FP32 in TMEM, where the chunk's decay is applied to them; what comes with
+//    the additions inside the tensor cores leaves the state of long prompts 2e-6 to
+//    4e-6 off.
+//  - of o's terms each meets one rounding to BF16 (2^-8), like its result: the masked
+//    products as the operand of V's, the state as that of Q's.  Two terms of each would
+//    need twice the products and the TMEM columns that the state's terms take.
+//  - G is summed in FP64.  An exponent goes to FP32: of a decay x since a token 2^-24 of x;
+//    of the masked products, as a sum of two through a row of the same 32, 2^-24 of the
+//    decay over up to 31 tokens each: with log-decays of 0 to -150 2^-11 at most (2^-11.5 of the
+//    factor), with growth 2^-23 of what 31 tokens grow by.
 //
 // A CTA walks 64 columns of one value head through one segment of a sequence.
 // Long sequences are cut into segments of L tokens that are walked at the same time:
@@ -349,8 +359,8 @@ int launch_few(const DecayParams& P, cudaStream_t st) {
 // segment's chunks are walked from its end, so that all decays are known and no
 // product waits for another.
 //
-// What bounds it: 32768 tokens of 32 heads of 128 x 128 (16 of q and k) take 475 us, of these
-// STATES 0.31, the join 0.02 and the walk 0.67.  A walk's chunk takes about 4800 cycles: two
+// What bounds it: 32768 tokens of 32 heads of 128 x 128 (16 of q and k) take 483-530 us (by the card
+// and its power limit), of these STATES 0.31, the join 0.02 and the walk 0.67.  A walk's chunk takes about 4800 cycles: two
 // chains (Q Kᵀ - decayed - times V, and the state out of TMEM - Q S - Kᵀ Ṽ) that meet in
 // every chunk, each a row of waits of some hundred cycles, over 400 KB of shared-memory
 // traffic (3100 cycles); a chunk of STATES takes 2040, as long as its decays' sums, its

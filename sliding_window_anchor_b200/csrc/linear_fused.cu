@@ -197,9 +197,10 @@ __device__ __forceinline__ void copy_rows(const FusedParams& P, const unsigned c
 // rows (rows g and g + 8, columns 8c..8c+7 of the step, g = lane/4, c = lane%4)
 // and 16 bytes of token g, and feeds them unchanged to two m16n8k16 products
 // (a K column meets the same K column on both operands, so their order does not
-// matter).  The K slices of a block's warps are added in a fixed order.  HBM bounds it:
-// 1 x 2560 x 4096 takes 7.4 us (2.8 TB/s; launch and ramp are half of it), gated
-// 1 x 2*6912 x 2560 14-18 us (70.8 MB; 4.0-4.9 TB/s).
+// matter).  The K slices of a block's warps are added in a fixed order.  HBM bounds it, with
+// the launch, the ramp and the few SMs that hold two blocks: with weights outside L2
+// 1 x 2560 x 4096 takes 7.4 us (2.8 TB/s; 6.4 with them in L2), gated 1 x 2*6912 x 2560
+// 15-18 us (70.8 MB; 3.9-4.7 TB/s).
 constexpr int FV_TOKENS = 8;
 constexpr int FV_MAXW = 8;
 
@@ -333,11 +334,12 @@ int launch_few(const FusedParams& P, cudaStream_t st) {
 // one tile, leave their FP32 sums in shared memory, and each adds up a part of
 // the tile over distributed shared memory, in the order of the shares.
 //
-// The tensor cores bound large products: 8192 x 10240 x 2560 takes 280 us (1.53 PFLOP/s;
-// the library's product alone 277), gated 4096 x 2*10240 x 2560 284.  Middling ones are
-// bound by what surrounds the tile: of 512 x 2560 x 4096 (17.2 us) 6.5 us are its
-// products at the tensor cores' rate; the launch, the ring's first fill from HBM, the
-// joining of the shares and the epilogue follow one another around them.
+// The tensor cores bound large products, with the power limit: 8192 x 10240 x 2560 takes 283 us
+// (1.52 PFLOP/s; the library's product alone 304 beside it) to 343 in a long run of calls
+// (1.25), gated 4096 x 2*10240 x 2560 274-326.  Middling ones are bound by what surrounds the
+// tile: of 512 x 2560 x 4096 (17.5 us with weights outside L2, 23.1 with a residual from
+// there too) 6.5 us are its products at the tensor cores' rate; the launch, the ring's first
+// fill, the joining of the shares and the epilogue follow one another around them.
 //
 // Per CTA: warp 8 — TMA; warp 9 — TMEM and, in a pair's even CTA, the MMAs;
 // warps 0-7 — the epilogue: warp w has the TMEM lanes (tokens) of quadrant w % 4
@@ -730,8 +732,9 @@ __global__ void __launch_bounds__(DN_THREADS, 1) k_dense(const __grid_constant__
 // fetched once for all of them.  In the gated product a CTA's 128 rows are 64 of w_gate and
 // the same 64 of w_up.  A pair has one tile.  Its sums go to shared memory, which the
 // operands need no more, and from there out, four features of a token a thread.  The weights'
-// stream and the tensor cores bound it about alike: gated 300 x 2*9000 x 2560 takes 27 us
-// (tiles of 256 tokens: 35; 92 MB of weights at 3.4 TB/s, 1.0 PFLOP/s).
+// stream and the tensor cores bound it about alike: gated 300 x 2*9000 x 2560 took 27 us
+// where tiles of 256 tokens took 35 (92 MB of weights at 3.4 TB/s, 1.0 PFLOP/s); cards
+// differ, 27-42 us with weights partly in L2 and 29-44 with weights outside it.
 struct ColumnsParams {
   CUtensorMap x_map;          // x [T][K], box 64 x nacc / 2
   CUtensorMap w_map, w2_map;  // weights [F][K], box 64 x 128 (gated: 64)
